@@ -15,6 +15,11 @@ Shapes (bf16 unless noted):
              written to rows [start, start+n) of the caches
     decode:  q [B, 64, 64] (un-rotated), kcache/vcache [B, L, 8, 64]
              (keys rotated), sinks fp32 [64], lengths int32 [B] -> out [B, 64, 64]
+    paged_append: k/v [B, n, 8, 64] into pages [num_pages, page_size, 8, 64] (bf16, or
+             float8_e4m3fn with scales fp32 [num_pages, 8]), found through
+             table int32 [B, max_pages]; lengths int32 [B] count the new tokens
+    paged_attention: q [B, n, 64, 64], the n newest tokens of each sequence, over
+             its pages -> out [B, n, 64, 64] ([B, 64, 64] for q [B, 64, 64])
 ``window <= 0`` is full causal; ``window = W > 0`` the W-key sliding window.
 ``rope="yarn"`` selects the library's YaRN rotation (factor 32 over a
 4096-token original context) in place of plain RoPE; a cache filled with one
@@ -29,7 +34,8 @@ import torch
 
 __all__ = ["prefill", "prefill_lse", "prefill_backward", "decode", "decode_noalloc",
            "prefill_workspace_bytes",
-           "decode_workspace_bytes", "prefill_chunk", "check", "debug_wait_timeout", "init", "rope_table",
+           "decode_workspace_bytes", "prefill_chunk", "paged_append", "paged_attention",
+           "paged_attention_workspace_bytes", "check", "debug_wait_timeout", "init", "rope_table",
            "library_path", "GptossAttnError", "NUM_HEADS", "NUM_KV_HEADS", "HEAD_DIM",
            "MAX_POSITION"]
 
@@ -37,6 +43,7 @@ NUM_HEADS = 64
 NUM_KV_HEADS = 8
 HEAD_DIM = 64
 MAX_POSITION = 131072
+PAGE_SIZES = (16, 32, 64, 128)
 ABI_VERSION = 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +57,19 @@ class GptossAttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__("%s failed: %s (status %d)" % (what, _status_string(status), status))
+
+
+class _PagedCache(ctypes.Structure):
+    """gptoss_attn_paged_cache of the C header."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("type", ctypes.c_int32)]
+
+
+_PAGE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
 
 def library_path() -> str:
@@ -102,6 +122,19 @@ def _load():
     lib.gptoss_attn_prefill_backward.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                                  vp, i32, i32, vp, sz, vp]
     lib.gptoss_attn_prefill_backward.restype = i32
+    cp, i64 = ctypes.POINTER(_PagedCache), ctypes.c_int64
+    lib.gptoss_attn_paged_append.argtypes = [cp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, i32,
+                                             i32, i32, vp]
+    lib.gptoss_attn_paged_append.restype = i32
+    lib.gptoss_attn_paged_append_yarn.argtypes = lib.gptoss_attn_paged_append.argtypes
+    lib.gptoss_attn_paged_append_yarn.restype = i32
+    lib.gptoss_attn_paged_attention_workspace_bytes.argtypes = [i32, i32]
+    lib.gptoss_attn_paged_attention_workspace_bytes.restype = sz
+    lib.gptoss_attn_paged_attention.argtypes = [cp, vp, i64, i64, vp, vp, vp, vp, i32, vp, i32,
+                                                i32, i32, vp, sz, vp]
+    lib.gptoss_attn_paged_attention.restype = i32
+    lib.gptoss_attn_paged_attention_yarn.argtypes = lib.gptoss_attn_paged_attention.argtypes
+    lib.gptoss_attn_paged_attention_yarn.restype = i32
     if lib.gptoss_attn_abi_version() != ABI_VERSION:
         raise ImportError("%s has ABI %d, expected %d" % (path, lib.gptoss_attn_abi_version(),
                                                           ABI_VERSION))
@@ -454,6 +487,158 @@ def decode_noalloc(q, kcache, vcache, sinks, lengths, window: int = 0, out=None,
     st = fn(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), sinks.data_ptr(),
             lengths.data_ptr(), int(window), out.data_ptr(), B, L, _stream_handle(stream))
     _raise(st, "gptoss_attn_decode_noalloc")
+    return out
+
+
+def _heads_at(t: torch.Tensor, heads: int, name: str, device) -> torch.Tensor:
+    """A bf16 [B, n, heads, 64] whose heads and elements are contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != HEAD_DIM:
+        raise ValueError("%s must be [B, n, %d, 64], got %s" % (name, heads, tuple(t.shape)))
+    if t.stride(3) != 1 or t.stride(2) != HEAD_DIM:
+        raise ValueError("%s must have contiguous heads, got strides %s" % (name, t.stride()))
+    return t
+
+
+def _step(t: torch.Tensor, dim: int) -> int:
+    """Stride of a dimension; 0 where there is nothing to step to."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _paged_cache(kpages, vpages, kscales, vscales, device) -> _PagedCache:
+    """Checks the pages (any strides with contiguous elements) and their scales."""
+    if kpages.dtype not in _PAGE_TYPES:
+        raise TypeError("kpages must be bfloat16 or float8_e4m3fn, got %s" % kpages.dtype)
+    if kpages.dim() != 4 or kpages.shape[1] not in PAGE_SIZES or \
+            kpages.shape[2] != NUM_KV_HEADS or kpages.shape[3] != HEAD_DIM:
+        raise ValueError("kpages must be [num_pages, 16|32|64|128, 8, 64], got %s"
+                         % (tuple(kpages.shape),))
+    if vpages.dtype != kpages.dtype:
+        raise TypeError("vpages must be %s, got %s" % (kpages.dtype, vpages.dtype))
+    stride = kpages.stride()
+    if vpages.shape != kpages.shape or vpages.stride() != stride:
+        raise ValueError("vpages must have the shape and strides of kpages")
+    if stride[3] != 1:
+        raise ValueError("the pages' elements must be contiguous, got strides %s" % (stride,))
+    for name, t in (("kpages", kpages), ("vpages", vpages)):
+        if t.device != device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    num_pages, page_size = kpages.shape[0], kpages.shape[1]
+    if kpages.dtype == torch.bfloat16:
+        if kscales is not None or vscales is not None:
+            raise ValueError("bf16 pages take no scales")
+        ks = vs = None
+    else:
+        for name, t in (("kscales", kscales), ("vscales", vscales)):
+            if t is None:
+                raise ValueError("float8_e4m3fn pages need %s" % name)
+            if tuple(_dev(t, torch.float32, name, device).shape) != (num_pages, NUM_KV_HEADS):
+                raise ValueError("%s must be [%d, 8], got %s" % (name, num_pages, tuple(t.shape)))
+        ks, vs = kscales.data_ptr(), vscales.data_ptr()
+    return _PagedCache(kpages.data_ptr(), vpages.data_ptr(), ks, vs, stride[0], stride[1],
+                       stride[2], num_pages, page_size, _PAGE_TYPES[kpages.dtype])
+
+
+def _paged_int(t, shape, name: str, device):
+    if tuple(_dev(t, torch.int32, name, device).shape) != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _paged_device(t: torch.Tensor, what: str) -> torch.device:
+    if t.device.type != "cuda":
+        raise ValueError("%s takes device tensors" % what)
+    return t.device
+
+
+def paged_append(k, v, pos, kpages, vpages, table, lengths, counts=None, kscales=None,
+                 vscales=None, stream=None, rope: str = "plain") -> None:
+    """Append each sequence's newest tokens to its pages, keys rotated at `pos` [B, n].
+
+    Token t < counts[b] (default n) goes to index lengths[b] - counts[b] + t of
+    sequence b: page table[b, index // page_size], slot index % page_size. k and v
+    may be slices of a fused projection. In float8_e4m3fn pages a page's scales
+    (a power of two per kv head) follow the largest value that it holds, and are
+    written to kscales / vscales [num_pages, 8]. Device tensors only."""
+    device = _paged_device(k, "paged_append")
+    _heads_at(k, NUM_KV_HEADS, "k", device)
+    _heads_at(v, NUM_KV_HEADS, "v", device)
+    if v.shape != k.shape:
+        raise ValueError("v must be %s, got %s" % (tuple(k.shape), tuple(v.shape)))
+    B, n = k.shape[0], k.shape[1]
+    cache = _paged_cache(kpages, vpages, kscales, vscales, device)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_pages], got %s" % (tuple(table.shape),))
+    max_pages = table.shape[1]
+    # the tensors themselves stay referenced here until the kernel is enqueued
+    table_ptr = _paged_int(table, (B, max_pages), "table", device)
+    pos_ptr = _paged_int(pos, (B, n), "pos", device)
+    lengths_ptr = _paged_int(lengths, (B,), "lengths", device)
+    counts_ptr = None if counts is None else _paged_int(counts, (B,), "counts", device)
+    lib = _load()
+    fn = lib.gptoss_attn_paged_append_yarn if _rope(rope) else lib.gptoss_attn_paged_append
+    with torch.cuda.device(device):
+        st = fn(cache, k.data_ptr(), v.data_ptr(), _step(k, 0), _step(k, 1), _step(v, 0),
+                _step(v, 1), pos_ptr, table_ptr, lengths_ptr, counts_ptr, B, n, max_pages,
+                _stream_handle(stream))
+    _raise(st, "gptoss_attn_paged_append")
+
+
+def paged_attention_workspace_bytes(batch: int, n: int) -> int:
+    return int(_load().gptoss_attn_paged_attention_workspace_bytes(batch, n))
+
+
+def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, pos=None,
+                    kscales=None, vscales=None, out=None, workspace=None, stream=None,
+                    rope: str = "plain") -> torch.Tensor:
+    """Attention of the n = q.shape[1] newest tokens of each sequence over its pages
+    (q [B, 64, 64]: one token). Token t has index lengths[b] - n + t, sees the keys up
+    to itself (the last `window` of them if window > 0), and is rotated at `pos`
+    [B, n], by default its index; its own key and value are in the pages already.
+    Table entries of pages without visible keys may be unset. Device tensors only."""
+    device = _paged_device(q, "paged_attention")
+    single = q.dim() == 3
+    q4 = _heads_at(q.unsqueeze(1) if single else q, NUM_HEADS, "q", device)
+    B, n = q4.shape[0], q4.shape[1]
+    cache = _paged_cache(kpages, vpages, kscales, vscales, device)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_pages], got %s" % (tuple(table.shape),))
+    max_pages = table.shape[1]
+    # the tensors themselves stay referenced here: their memory must not serve the
+    # allocations below
+    table_ptr = _paged_int(table, (B, max_pages), "table", device)
+    lengths_ptr = _paged_int(lengths, (B,), "lengths", device)
+    pos_ptr = None if pos is None else _paged_int(pos, (B, n), "pos", device)
+    if tuple(_dev(sinks, torch.float32, "sinks", device).shape) != (NUM_HEADS,):
+        raise ValueError("sinks must be [64], got %s" % (tuple(sinks.shape),))
+    shape = (B, NUM_HEADS, HEAD_DIM) if single else (B, n, NUM_HEADS, HEAD_DIM)
+    if out is not None and tuple(_dev(out, torch.bfloat16, "out", device).shape) != shape:
+        raise ValueError("out must be %s, got %s" % (list(shape), tuple(out.shape)))
+    if workspace is not None and not (workspace.device == device and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    lib = _load()
+    fn = lib.gptoss_attn_paged_attention_yarn if _rope(rope) else lib.gptoss_attn_paged_attention
+    with torch.cuda.device(device):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        made = []
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+            made.append(out)
+        if workspace is None:
+            workspace = torch.empty(paged_attention_workspace_bytes(B, n), dtype=torch.uint8,
+                                    device=device)
+            made.append(workspace)
+        if stream is not None:
+            for t in made:  # the current stream's, but `stream` uses them
+                t.record_stream(s)
+        st = fn(cache, q4.data_ptr(), _step(q4, 0), _step(q4, 1), pos_ptr, table_ptr,
+                sinks.data_ptr(), lengths_ptr, int(window), out.data_ptr(), B, n, max_pages,
+                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                s.cuda_stream)
+    _raise(st, "gptoss_attn_paged_attention")
     return out
 
 

@@ -6,6 +6,7 @@
 
 #include "gptoss_attn.h"
 #include "internal.h"
+#include "paged.h"
 #include "tmap.h"
 
 namespace {
@@ -119,6 +120,7 @@ const char* gptoss_attn_status_string(int status) {
     case GPTOSS_ATTN_ERR_DEVICE_TIMEOUT: return "a kernel pipeline wait timed out";
     case GPTOSS_ATTN_ERR_BAD_POSITION: return "a rotary position was outside [0, 131072)";
     case GPTOSS_ATTN_ERR_BAD_LENGTH: return "a decode length was outside [0, max_len]";
+    case GPTOSS_ATTN_ERR_BAD_PAGE: return "a page number was outside [0, num_pages)";
     default: return "unknown status";
   }
 }
@@ -507,6 +509,198 @@ int gptoss_attn_prefill_backward(const void* q, const void* k, const void* v, co
                                                               : GPTOSS_ATTN_ERR_LAUNCH;
 }
 
+// Checks a paged cache and its table, and fills in the kernels' view of it.
+static int paged_view(const gptoss_attn_paged_cache* c, int max_pages, PagedCache* view) {
+  if (!c || !c->k || !c->v) return GPTOSS_ATTN_ERR_NULL_PTR;
+  int log2 = 4;
+  while (log2 < 8 && (1 << log2) != c->page_size) ++log2;
+  if (log2 == 8 || c->num_pages < 1 || max_pages < 1 || max_pages > (kMaxPosition >> log2) ||
+      (c->type != GPTOSS_ATTN_PAGES_BF16 && c->type != GPTOSS_ATTN_PAGES_E4M3))
+    return GPTOSS_ATTN_ERR_BAD_SHAPE;
+  const bool fp8 = c->type == GPTOSS_ATTN_PAGES_E4M3;
+  if (fp8 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale))
+    return fp8 ? GPTOSS_ATTN_ERR_NULL_PTR : GPTOSS_ATTN_ERR_BAD_SHAPE;
+  const int64_t unit = fp8 ? 16 : 8;  // elements in 16 bytes
+  const int64_t strides[3] = {c->page_stride, c->token_stride, c->head_stride};
+  for (int64_t s : strides) {
+    // positive, and no more than a tensor map's 40 bits of bytes
+    if (s < kHeadDim || s >= (int64_t{1} << 38)) return GPTOSS_ATTN_ERR_BAD_SHAPE;
+    if (s % unit) return GPTOSS_ATTN_ERR_BAD_ALIGN;
+  }
+  if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->v_scale) & 3u))
+    return GPTOSS_ATTN_ERR_BAD_ALIGN;
+  view->k = static_cast<uint8_t*>(c->k);
+  view->v = static_cast<uint8_t*>(c->v);
+  view->k_scale = c->k_scale;
+  view->v_scale = c->v_scale;
+  view->page_stride = c->page_stride;
+  view->token_stride = c->token_stride;
+  view->head_stride = c->head_stride;
+  view->num_pages = c->num_pages;
+  view->page_log2 = log2;
+  view->fp8 = fp8;
+  return GPTOSS_ATTN_OK;
+}
+
+static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+static int paged_append_impl(const gptoss_attn_paged_cache* cache, const void* k, const void* v,
+                             int64_t k_batch, int64_t k_token, int64_t v_batch, int64_t v_token,
+                             const int32_t* pos, const int32_t* table, const int32_t* len,
+                             const int32_t* count, int batch, int n, int max_pages,
+                             cudaStream_t stream, Rope rope) {
+  if (!k || !v || !pos || !table || !len) return GPTOSS_ATTN_ERR_NULL_PTR;
+  PagedAppendArgs a;
+  int st = paged_view(cache, max_pages, &a.cache);
+  if (st != GPTOSS_ATTN_OK) return st;
+  if (batch < 1 || batch > 65535 || n < 1 || n > kMaxPosition) return GPTOSS_ATTN_ERR_BAD_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || ((k_batch | k_token | v_batch | v_token) & 7) ||
+      misaligned4(pos) || misaligned4(table) || misaligned4(len) || misaligned4(count))
+    return GPTOSS_ATTN_ERR_BAD_ALIGN;
+  int dev = 0;
+  st = current_device(&dev);
+  if (st == GPTOSS_ATTN_OK) st = ensure_state(dev, rope);
+  if (st != GPTOSS_ATTN_OK) return st;
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_batch = k_batch;
+  a.k_token = k_token;
+  a.v_batch = v_batch;
+  a.v_token = v_token;
+  a.pos = pos;
+  a.table = table;
+  a.len = len;
+  a.count = count;
+  a.rope = table_of(dev, rope);
+  a.err = err_word(dev, stream);
+  a.batch = batch;
+  a.n = n;
+  a.max_pages = max_pages;
+  a.max_len = max_pages << a.cache.page_log2;
+  return launch_paged_append(a, stream) == cudaSuccess ? GPTOSS_ATTN_OK : GPTOSS_ATTN_ERR_LAUNCH;
+}
+
+int gptoss_attn_paged_append(const gptoss_attn_paged_cache* cache, const void* k, const void* v,
+                             int64_t k_batch_stride, int64_t k_token_stride,
+                             int64_t v_batch_stride, int64_t v_token_stride, const int32_t* pos,
+                             const int32_t* table, const int32_t* len, const int32_t* count,
+                             int batch, int n, int max_pages, cudaStream_t stream) {
+  return paged_append_impl(cache, k, v, k_batch_stride, k_token_stride, v_batch_stride,
+                           v_token_stride, pos, table, len, count, batch, n, max_pages, stream,
+                           Rope::kPlain);
+}
+
+int gptoss_attn_paged_append_yarn(const gptoss_attn_paged_cache* cache, const void* k,
+                                  const void* v, int64_t k_batch_stride, int64_t k_token_stride,
+                                  int64_t v_batch_stride, int64_t v_token_stride,
+                                  const int32_t* pos, const int32_t* table, const int32_t* len,
+                                  const int32_t* count, int batch, int n, int max_pages,
+                                  cudaStream_t stream) {
+  return paged_append_impl(cache, k, v, k_batch_stride, k_token_stride, v_batch_stride,
+                           v_token_stride, pos, table, len, count, batch, n, max_pages, stream,
+                           Rope::kYarn);
+}
+
+static bool paged_sizes_ok(int batch, int n) {
+  return batch >= 1 && n >= 1 && static_cast<int64_t>(batch) * n <= kMaxPosition;
+}
+
+// Rows of queries of one call.
+static int paged_rows(int batch, int n) {
+  const int nt = paged_row_tokens(n);
+  return batch * ((n + nt - 1) / nt);
+}
+
+size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n) {
+  size_t off[3];
+  return paged_sizes_ok(batch, n) ? paged_workspace_bytes(paged_rows(batch, n), n, off) : 0;
+}
+
+static int paged_attention_impl(const gptoss_attn_paged_cache* cache, const void* q,
+                                int64_t q_batch, int64_t q_token, const int32_t* pos,
+                                const int32_t* table, const float* sinks, const int32_t* len,
+                                int window, void* out, int batch, int n, int max_pages,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream,
+                                Rope rope) {
+  if (!q || !table || !sinks || !len || !out || !workspace) return GPTOSS_ATTN_ERR_NULL_PTR;
+  PagedAttentionArgs a;
+  int st = paged_view(cache, max_pages, &a.cache);
+  if (st != GPTOSS_ATTN_OK) return st;
+  if (!paged_sizes_ok(batch, n)) return GPTOSS_ATTN_ERR_BAD_SHAPE;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || ((q_batch | q_token) & 7) ||
+      misaligned4(pos) || misaligned4(table) || misaligned4(sinks) || misaligned4(len))
+    return GPTOSS_ATTN_ERR_BAD_ALIGN;
+  a.rows = paged_rows(batch, n);
+  size_t off[3];
+  if (workspace_bytes < paged_workspace_bytes(a.rows, n, off))
+    return GPTOSS_ATTN_ERR_SMALL_WORKSPACE;
+  int dev = 0;
+  st = current_device(&dev);
+  if (st == GPTOSS_ATTN_OK) st = ensure_state(dev, rope);
+  if (st != GPTOSS_ATTN_OK) return st;
+
+  const PagedCache& c = a.cache;
+  PagedMaps maps;
+  const uint64_t elem = c.fp8 ? 1 : 2;
+  const uint32_t P = 1u << c.page_log2;
+  const uint64_t dims[4] = {kHeadDim, kNumKvHeads, P, static_cast<uint64_t>(c.num_pages)};
+  const uint64_t str[3] = {c.head_stride * elem, c.token_stride * elem, c.page_stride * elem};
+  const uint32_t box[4] = {kHeadDim, 1, P < kPagedTile ? P : kPagedTile, 1};
+  const bool made = c.fp8 ? make_tmap_u8_4d(&maps.k, c.k, dims, str, box) &&
+                                make_tmap_u8_4d(&maps.v, c.v, dims, str, box)
+                          : make_tmap_bf16_4d(&maps.k, c.k, dims, str, box) &&
+                                make_tmap_bf16_4d(&maps.v, c.v, dims, str, box);
+  if (!made) return GPTOSS_ATTN_ERR_TENSOR_MAP;
+
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_batch = q_batch;
+  a.q_token = q_token;
+  a.pos = pos;
+  a.table = table;
+  a.sinks = sinks;
+  a.len = len;
+  a.rope = table_of(dev, rope);
+  a.out = static_cast<uint16_t*>(out);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws + off[0]);
+  a.part_ml = reinterpret_cast<float2*>(ws + off[1]);
+  a.meta = reinterpret_cast<int2*>(ws + off[2]);
+  a.err = err_word(dev, stream);
+  a.batch = batch;
+  a.n = n;
+  a.max_pages = max_pages;
+  a.max_len = max_pages << c.page_log2;
+  // A window covering the longest sequence is full causal.
+  a.window = window > 0 && window < a.max_len ? window : 0;
+  a.groups = a.rows / batch;
+  a.target = paged_target(n);
+  return launch_paged_attention(maps, a, stream) == cudaSuccess ? GPTOSS_ATTN_OK
+                                                                : GPTOSS_ATTN_ERR_LAUNCH;
+}
+
+int gptoss_attn_paged_attention(const gptoss_attn_paged_cache* cache, const void* q,
+                                int64_t q_batch_stride, int64_t q_token_stride,
+                                const int32_t* pos, const int32_t* table, const float* sinks,
+                                const int32_t* len, int window, void* out, int batch, int n,
+                                int max_pages, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  return paged_attention_impl(cache, q, q_batch_stride, q_token_stride, pos, table, sinks, len,
+                              window, out, batch, n, max_pages, workspace, workspace_bytes, stream,
+                              Rope::kPlain);
+}
+
+int gptoss_attn_paged_attention_yarn(const gptoss_attn_paged_cache* cache, const void* q,
+                                     int64_t q_batch_stride, int64_t q_token_stride,
+                                     const int32_t* pos, const int32_t* table, const float* sinks,
+                                     const int32_t* len, int window, void* out, int batch, int n,
+                                     int max_pages, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+  return paged_attention_impl(cache, q, q_batch_stride, q_token_stride, pos, table, sinks, len,
+                              window, out, batch, n, max_pages, workspace, workspace_bytes, stream,
+                              Rope::kYarn);
+}
+
 int gptoss_attn_debug_wait_timeout(unsigned timeout_us, cudaStream_t stream) {
   if (timeout_us == 0 || timeout_us > 2000000u) return GPTOSS_ATTN_ERR_BAD_SHAPE;
   int dev = 0;
@@ -540,6 +734,7 @@ int gptoss_attn_check(cudaStream_t stream) {
   if (h & kErrTimeout) return GPTOSS_ATTN_ERR_DEVICE_TIMEOUT;
   if (h & kErrPosition) return GPTOSS_ATTN_ERR_BAD_POSITION;
   if (h & kErrLength) return GPTOSS_ATTN_ERR_BAD_LENGTH;
+  if (h & kErrPage) return GPTOSS_ATTN_ERR_BAD_PAGE;
   return GPTOSS_ATTN_OK;
 }
 

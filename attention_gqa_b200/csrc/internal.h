@@ -20,6 +20,7 @@ constexpr double kRopeTheta = 150000.0;
 constexpr int kErrTimeout = 1;
 constexpr int kErrPosition = 2;
 constexpr int kErrLength = 4;
+constexpr int kErrPage = 8;
 
 // Pipeline waits give up after this long (a healthy wait lasts microseconds).
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
@@ -145,6 +146,66 @@ void backward_plan(BackwardArgs* args, int target_ctas);
 // the rotated q and k written to the workspace before).
 cudaError_t launch_backward(const BackwardMaps& maps, const BackwardArgs& args, int num_sms,
                             cudaStream_t stream);
+
+// A paged key/value cache. Page p, token t of the page, kv head h, element d lies at
+// p * page_stride + t * token_stride + h * head_stride + d (elements, K and V alike).
+struct PagedCache {
+  uint8_t* k;              // bf16 or e4m3
+  uint8_t* v;
+  float* k_scale;          // [num_pages][8], e4m3 only
+  float* v_scale;
+  int64_t page_stride, token_stride, head_stride;
+  int num_pages;
+  int page_log2;           // log2 of the tokens per page
+  bool fp8;
+};
+
+struct PagedAppendArgs {
+  PagedCache cache;
+  const uint16_t* k;       // bf16, heads and elements contiguous
+  const uint16_t* v;
+  int64_t k_batch, k_token, v_batch, v_token;  // strides of k and v in elements
+  const int32_t* pos;      // [B][n]
+  const int32_t* table;    // [B][max_pages]
+  const int32_t* len;      // [B], with the new tokens
+  const int32_t* count;    // [B] new tokens of each sequence, or nullptr: n
+  const float2* rope;
+  int* err;
+  int batch, n, max_pages, max_len;
+};
+
+cudaError_t launch_paged_append(const PagedAppendArgs& args, cudaStream_t stream);
+
+struct PagedAttentionArgs {
+  PagedCache cache;
+  const uint16_t* q;       // bf16, heads and elements contiguous, un-rotated
+  int64_t q_batch, q_token;
+  const int32_t* pos;      // [B][n] rotary positions, or nullptr: the tokens' indices
+  const int32_t* table;    // [B][max_pages]
+  const float* sinks;      // [64]
+  const int32_t* len;      // [B]
+  const float2* rope;
+  uint16_t* out;           // [B][n][64][64] bf16
+  float* part_o;           // [part][8][NT * 8][64]: unnormalised sums of a chunk
+  float2* part_ml;         // [part][8][NT * 8] (max in log2 units, sum)
+  int2* meta;              // [rows] (first part, chunks)
+  int* err;
+  int batch, n, max_pages, max_len, window;
+  int groups;              // rows (token groups) per sequence
+  int rows;                // batch * groups
+  int target;              // chunks aimed for
+};
+
+struct PagedMaps {
+  CUtensorMap k, v;        // boxes (64, 1, min(page, 64), 1)
+};
+
+// Query tokens a row holds, chunks aimed for, and the workspace they need.
+int paged_row_tokens(int n);
+int paged_target(int n);
+size_t paged_workspace_bytes(int64_t rows, int n, size_t off[3]);
+cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& args,
+                                   cudaStream_t stream);
 
 // Decode split planning shared by the workspace query and the launch.
 void decode_plan(int batch, int max_len, int window, int* nsplit, int* chunk);

@@ -1,0 +1,89 @@
+// The paged key/value cache: what its host entry points and kernels agree on.
+//
+// The arithmetic here (which keys a row of queries sees, how the work is cut
+// into chunks, where a token lies, which scale a page gets) is plain C++ that
+// also compiles without CUDA, so it is tested on the CPU.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define GQA_HD __host__ __device__ __forceinline__
+#else
+#define GQA_HD inline
+#endif
+
+namespace gqa {
+
+constexpr int kPagedTile = 64;  // keys per tile of the attention kernel
+
+// Keys [lo, hi) that some token of one row of queries sees. A row is up to
+// `nt` tokens of one sequence, the tokens t0 .. of the n newest; token t sits at
+// index len - n + t (a negative index is no token and sees nothing).
+GQA_HD void paged_row_range(int len, int n, int t0, int nt, int window, int* lo, int* hi) {
+  const int last = t0 + nt < n ? t0 + nt : n;
+  const int first_idx = len - n + t0;
+  *hi = len - n + last > 0 ? len - n + last : 0;
+  *lo = window > 0 && first_idx - window + 1 > 0 ? first_idx - window + 1 : 0;
+}
+
+GQA_HD int paged_row_tiles(int lo, int hi) {
+  return hi > lo ? (hi - 1) / kPagedTile - lo / kPagedTile + 1 : 0;
+}
+
+// Tiles per chunk when all rows together have `total` tiles: about `target`
+// chunks, but no chunk shorter than four tiles while a single wave of
+// CTAs (a quarter of the target) takes the whole work in chunks of four.
+GQA_HD int paged_chunk_tiles(int64_t total, int target) {
+  const int64_t many = (total + target - 1) / target;
+  int64_t one = (total * 4 + target - 1) / target;
+  if (one > 4) one = 4;
+  const int64_t c = many > one ? many : one;
+  return c < 1 ? 1 : static_cast<int>(c);
+}
+
+// Chunks of one row (a row without keys has one too: it writes the zeros).
+GQA_HD int paged_row_chunks(int tiles, int chunk) {
+  return tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
+}
+
+// Chunks of a whole call are at most this many: sum of max(1, ceil(tiles/c))
+// with c >= total/target.
+GQA_HD int64_t paged_max_chunks(int64_t rows, int target) { return rows + target; }
+
+// Chunks of rows that have more than one: those leave partial sums in the
+// workspace. Such a row has more than c tiles, so ceil(tiles/c) < 2 tiles/c.
+GQA_HD int64_t paged_max_parts(int target) { return 2 * static_cast<int64_t>(target); }
+
+// Tiles [*a, *b) of a row's `tiles` that chunk `i` of `chunks` takes.
+GQA_HD void paged_chunk_range(int tiles, int chunks, int i, int* a, int* b) {
+  *a = static_cast<int>(static_cast<int64_t>(tiles) * i / chunks);
+  *b = static_cast<int>(static_cast<int64_t>(tiles) * (i + 1) / chunks);
+}
+
+GQA_HD bool paged_page_ok(int page, int num_pages) { return page >= 0 && page < num_pages; }
+
+// Whether an append of `count` of at most `n` tokens that ends at `len` stays
+// inside a sequence of max_len tokens.
+GQA_HD bool paged_append_ok(int len, int count, int n, int max_len) {
+  return count >= 0 && count <= n && len >= count && len <= max_len;
+}
+
+// Exponents a page's scale may have: 448 * 2^120 holds every finite bf16, and
+// values below 2^-64 need no finer steps.
+constexpr int kScaleLow = -64;
+constexpr int kScaleHigh = 120;
+
+// Bits of the least power of two 2^e with `largest` <= 448 * 2^e, e limited to
+// [kScaleLow, kScaleHigh]; `largest_bits` are those of a finite fp32 >= 0.
+// 448 = 1.75 * 2^8: a value m * 2^x (1 <= m < 2) needs e = x - 8, or x - 7 above 1.75.
+GQA_HD uint32_t paged_scale_bits(uint32_t largest_bits) {
+  int e = static_cast<int>(largest_bits >> 23) - 127 - 8;
+  if ((largest_bits & 0x7FFFFFu) > 0x600000u) ++e;
+  if (e < kScaleLow) e = kScaleLow;
+  if (e > kScaleHigh) e = kScaleHigh;
+  return static_cast<uint32_t>(e + 127) << 23;
+}
+
+}  // namespace gqa

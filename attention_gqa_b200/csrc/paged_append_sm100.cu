@@ -1,0 +1,264 @@
+// Appending keys and values to a paged cache for sm_100a, keys rotated on the way.
+//
+// Token t of a sequence's `count` new ones sits at index i = len - count + t, in
+// page table[b][i / P] at slot i % P. bf16 pages take the rotated key (fp32
+// arithmetic from the fp64-built table, one rounding, as rope_rows_kernel does
+// it) and the value as given. e4m3 pages hold x / s with one scale s per page
+// and head, a power of two so that a later, larger scale moves the codes that
+// are there without rounding them again (but for those that get subnormal):
+//   s = max(s of the page's earlier tokens, least 2^e with max |x| <= 448 * 2^e).
+// Infinities saturate and NaN stays; neither decides the scale.
+//
+// Both kernels are bound by HBM: 256 bytes read per token and kv head, 256 (bf16)
+// or 128 (e4m3) written.
+#include "internal.h"
+#include "paged.h"
+#include "sm100_ptx.cuh"
+
+namespace gqa {
+namespace {
+
+// (cos, sin) of pairs 8c .. 8c+7 of a table row.
+struct Turn {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const float2* row, int chunk) {
+    const float4* t4 = reinterpret_cast<const float4*>(row + 8 * chunk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = __ldg(t4 + i);
+      c[2 * i] = t.x;
+      s[2 * i] = t.y;
+      c[2 * i + 1] = t.z;
+      s[2 * i + 1] = t.w;
+    }
+  }
+};
+
+// Elements 8c .. 8c+7 (lo) and 8c+32 .. 8c+39 (hi) of a head, as fp32.
+struct Halves {
+  float lo[8], hi[8];
+  __device__ __forceinline__ void unpack(const uint4& a, const uint4& h) {
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[2 * e] = bf16lo_to_f32(aw[e]);
+      lo[2 * e + 1] = bf16hi_to_f32(aw[e]);
+      hi[2 * e] = bf16lo_to_f32(hw[e]);
+      hi[2 * e + 1] = bf16hi_to_f32(hw[e]);
+    }
+  }
+  __device__ __forceinline__ void turn(const Turn& t) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = lo[e], h = hi[e];
+      lo[e] = fmaf(a, t.c[e], -h * t.s[e]);
+      hi[e] = fmaf(h, t.c[e], a * t.s[e]);
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// Table row of a token's position; one outside the table is reported and clamped.
+__device__ __forceinline__ const float2* table_row(const PagedAppendArgs& a, int b, int t) {
+  int p = __ldg(a.pos + static_cast<int64_t>(b) * a.n + t);
+  if (p < 0 || p >= kMaxPosition) {
+    atomicOr(a.err, kErrPosition);
+    p = p < 0 ? 0 : kMaxPosition - 1;
+  }
+  return a.rope + static_cast<int64_t>(p) * kRopePairs;
+}
+
+// Where a sequence's new tokens start and how many there are; a call that does
+// not fit its sequence is reported and appends nothing to it.
+__device__ __forceinline__ bool new_tokens(const PagedAppendArgs& a, int b, int* start,
+                                           int* count) {
+  const int len = __ldg(a.len + b);
+  const int c = a.count ? __ldg(a.count + b) : a.n;
+  if (!paged_append_ok(len, c, a.n, a.max_len)) {
+    atomicOr(a.err, kErrLength);
+    return false;
+  }
+  *start = len - c;
+  *count = c;
+  return true;
+}
+
+// One warp per token, four lanes per kv head: lane c of a head takes the 16-byte
+// chunks c and c+4, which the rotation pairs, of its key and of its value.
+__global__ void __launch_bounds__(256) append_bf16_kernel(const PagedAppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();  // lengths, tokens and pages may come from the kernel before
+  const int b = static_cast<int>(blockIdx.y);
+  const int t = static_cast<int>(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int head = lane >> 2, c = lane & 3;
+  int start, count;
+  if (t >= a.n || !new_tokens(a, b, &start, &count) || t >= count) return;
+  const PagedCache& pc = a.cache;
+  const int i = start + t;
+  const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + (i >> pc.page_log2));
+  const uint4* k4 = reinterpret_cast<const uint4*>(a.k + b * a.k_batch + t * a.k_token +
+                                                   head * kHeadDim);
+  const uint4* v4 = reinterpret_cast<const uint4*>(a.v + b * a.v_batch + t * a.v_token +
+                                                   head * kHeadDim);
+  const uint4 klo = __ldg(k4 + c), khi = __ldg(k4 + c + 4);
+  const uint4 vlo = __ldg(v4 + c), vhi = __ldg(v4 + c + 4);
+  Turn turn;
+  turn.load(table_row(a, b, t), c);
+  if (!paged_page_ok(page, pc.num_pages)) {
+    if (lane == 0) atomicOr(a.err, kErrPage);
+    return;
+  }
+  Halves x;
+  x.unpack(klo, khi);
+  x.turn(turn);
+  const int64_t at = page * pc.page_stride +
+                     (i & ((1 << pc.page_log2) - 1)) * pc.token_stride + head * pc.head_stride;
+  uint4* ko = reinterpret_cast<uint4*>(pc.k + 2 * at);
+  uint4* vo = reinterpret_cast<uint4*>(pc.v + 2 * at);
+  ko[c] = pack8(x.lo);
+  ko[c + 4] = pack8(x.hi);
+  vo[c] = vlo;
+  vo[c + 4] = vhi;
+}
+
+// Two fp32 values to two e4m3 codes (round to nearest even, saturating; NaN stays).
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint2 pack_e4m3x8(const float (&x)[8], float f) {
+  return make_uint2(pack_e4m3x2(x[0] * f, x[1] * f) | pack_e4m3x2(x[2] * f, x[3] * f) << 16,
+                    pack_e4m3x2(x[4] * f, x[5] * f) | pack_e4m3x2(x[6] * f, x[7] * f) << 16);
+}
+
+// The two values of two codes.
+__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  float lo, hi;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+  return make_float2(lo, hi);
+}
+
+__device__ __forceinline__ uint32_t move_e4m3x4(uint32_t codes, float f) {
+  const float2 a = unpack_e4m3x2(codes & 0xFFFFu), b = unpack_e4m3x2(codes >> 16);
+  return pack_e4m3x2(a.x * f, a.y * f) | pack_e4m3x2(b.x * f, b.y * f) << 16;
+}
+
+// A CTA per page that a sequence's new tokens touch, a warp per head of its keys
+// (warps 0-7) and of its values (8-15), so a page's scale is one warp's business.
+// A warp goes over its new rows twice, eight at a time (four lanes each): once
+// for the largest value, once to write the codes.
+__global__ void __launch_bounds__(512) append_e4m3_kernel(const PagedAppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int b = static_cast<int>(blockIdx.y);
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int head = warp & 7;
+  const bool is_v = warp >= 8;
+  const int sub = lane >> 2, c = lane & 3;
+  int start, count;
+  if (!new_tokens(a, b, &start, &count)) return;
+  const PagedCache& pc = a.cache;
+  const int P = 1 << pc.page_log2;
+  const int pi = (start >> pc.page_log2) + static_cast<int>(blockIdx.x);  // page of the sequence
+  const int base = pi << pc.page_log2;                                    // its first index
+  if (base >= start + count) return;
+  const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + pi);
+  if (!paged_page_ok(page, pc.num_pages)) {
+    if (threadIdx.x == 0) atomicOr(a.err, kErrPage);
+    return;
+  }
+  const int s0 = start > base ? start - base : 0;            // slots [s0, s1) are new
+  const int s1 = start + count - base < P ? start + count - base : P;
+  const uint16_t* src = is_v ? a.v + b * a.v_batch : a.k + b * a.k_batch;
+  const int64_t src_token = is_v ? a.v_token : a.k_token;
+  const int64_t at = page * pc.page_stride + head * pc.head_stride;
+  uint8_t* dst = (is_v ? pc.v : pc.k) + at;
+  float* scale = (is_v ? pc.v_scale : pc.k_scale) + static_cast<int64_t>(page) * kNumKvHeads + head;
+
+  // this lane's sixteen values of slot s
+  auto row = [&](int s, Halves* x) {
+    const int t = base + s - start;
+    const uint4* p4 = reinterpret_cast<const uint4*>(src + t * src_token + head * kHeadDim);
+    x->unpack(__ldg(p4 + c), __ldg(p4 + c + 4));
+    if (!is_v) {
+      Turn turn;
+      turn.load(table_row(a, b, t), c);
+      x->turn(turn);
+    }
+  };
+  float largest = 0.f;
+  for (int s = s0 + sub; s < s1; s += 8) {
+    Halves x;
+    row(s, &x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = fabsf(x.lo[e]), v = fabsf(x.hi[e]);
+      if (u < INFINITY) largest = fmaxf(largest, u);
+      if (v < INFINITY) largest = fmaxf(largest, v);
+    }
+  }
+  largest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(largest)));
+  float size = __uint_as_float(paged_scale_bits(__float_as_uint(largest)));
+  if (s0 > 0) {  // earlier tokens share the page
+    const float before = *scale;
+    if (before >= size) {
+      size = before;
+    } else {
+      const float f = before / size;
+      for (int s = sub; s < s0; s += 8) {
+        uint4* row4 = reinterpret_cast<uint4*>(dst + s * pc.token_stride) + c;
+        const uint4 w = *row4;
+        *row4 = make_uint4(move_e4m3x4(w.x, f), move_e4m3x4(w.y, f), move_e4m3x4(w.z, f),
+                           move_e4m3x4(w.w, f));
+      }
+    }
+  }
+  __syncwarp();  // every lane has read the scale that was there
+  if (lane == 0) *scale = size;
+  const float inv = 1.f / size;
+  for (int s = s0 + sub; s < s1; s += 8) {
+    Halves x;
+    row(s, &x);
+    uint2* row2 = reinterpret_cast<uint2*>(dst + s * pc.token_stride);
+    row2[c] = pack_e4m3x8(x.lo, inv);
+    row2[c + 4] = pack_e4m3x8(x.hi, inv);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  if (a.cache.fp8) {
+    // pages that n tokens can touch, wherever in a page they start
+    const int P = 1 << a.cache.page_log2;
+    cfg.gridDim = dim3(static_cast<unsigned>((a.n + P - 2) / P + 1), static_cast<unsigned>(a.batch));
+    cfg.blockDim = dim3(512);
+    return cudaLaunchKernelEx(&cfg, append_e4m3_kernel, a);
+  }
+  int warps = 1;
+  while (warps < 8 && warps < a.n) warps *= 2;
+  cfg.gridDim = dim3(static_cast<unsigned>((a.n + warps - 1) / warps),
+                     static_cast<unsigned>(a.batch));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
+  return cudaLaunchKernelEx(&cfg, append_bf16_kernel, a);
+}
+
+}  // namespace gqa

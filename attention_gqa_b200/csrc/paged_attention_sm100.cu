@@ -1,0 +1,808 @@
+// Attention of the newest tokens of each sequence over a paged key/value cache,
+// for sm_100a: grouped queries, sliding window and per-head sink as in the other
+// entry points; pages of bf16, or of e4m3 with a scale per page and kv head.
+//
+// Work. A row is up to NT consecutive query tokens of one sequence. Its visible
+// keys are cut into tiles of 64, and all rows' tiles into chunks of about equal
+// length (paged.h): every CTA finds its (row, chunk, kv head) by a scan over the
+// lengths, so the work follows the lengths on the device and not the capacity of
+// the table. Chunks of a row that has several leave partial sums, which the
+// combine kernel joins; a row's only chunk writes its output itself.
+//
+// Orientation. Products run transposed, keys (or head_dim) in the 16 rows of
+// mma.m16n8k16 and the 8 query heads of a group in its 8 columns:
+//   S^T = K Q^T, O^T = V^T P^T,
+// so one token wastes no half of an instruction, and K and V fragments serve all
+// NT tokens. Each of four warps takes 16 keys of every tile, with its own running
+// maximum; the warps join at the end.
+//
+// Precision. bf16 pages: q and p are split into two bf16 terms (the second product
+// costs tensor time that HBM leaves unused), so only the sums' fp32 and the output
+// round. e4m3 pages: codes are exact in f16, q is scaled by a power of two per head
+// and rounded to f16 (2^-12), and so is p. A page's value scale s_v joins the
+// exponent, w = 2^(x + log2 s_v - M), which keeps w in f16's range whatever the
+// scales are; the normaliser takes w / s_v in fp32.
+//
+// Bound by HBM for few tokens: 256 (bf16) or 128 (e4m3) bytes per key and head.
+#include <cfloat>
+#include <cmath>
+
+#include "internal.h"
+#include "paged.h"
+#include "sm100_ptx.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kWarps = 4;  // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kScaleLog2 = 0.125f * kLog2e;
+// The running maximum follows the scores only when one exceeds it by this much
+// (log2 units): p then stays below 2^8, and most tiles leave the sums alone.
+constexpr float kRescaleThreshold = 8.0f;
+// A running maximum below every score: 2^(kNoMax - x) is 0 for any finite x.
+constexpr float kNoMax = -FLT_MAX;
+
+template <bool kFp8>
+struct Shape {
+  static constexpr int kElem = kFp8 ? 1 : 2;
+  static constexpr int kStages = kFp8 ? 6 : 4;
+  static constexpr uint32_t kTileBytes = kPagedTile * kHeadDim * kElem;  // one of K or V
+};
+
+struct ScanSlot {
+  int row, split, chunks, part;
+};
+
+template <bool kFp8, int NT>
+struct Smem {
+  static constexpr uint32_t kK = 0;
+  static constexpr uint32_t kV = kK + Shape<kFp8>::kStages * Shape<kFp8>::kTileBytes;
+  static constexpr uint32_t kTiles = kV + Shape<kFp8>::kStages * Shape<kFp8>::kTileBytes;
+  // the warps' sums are joined where the tiles were
+  static constexpr uint32_t kMergeWarp = NT * kGroup * (kHeadDim + 2) * 4;
+  static constexpr uint32_t kMerge = 0;
+  static constexpr uint32_t kEnd0 = kTiles > kWarps * kMergeWarp ? kTiles : kWarps * kMergeWarp;
+  static constexpr uint32_t kQ = kEnd0;  // 16-bit [2][NT][8][64] (the second half: bf16 only)
+  static constexpr uint32_t kQExp = kQ + (kFp8 ? 1 : 2) * NT * kGroup * kHeadDim * 2;  // [NT][8]
+  static constexpr uint32_t kPage = kQExp + NT * kGroup * 4;  // float4 [stages][4 warps], e4m3
+  static constexpr uint32_t kBar = kPage + (kFp8 ? Shape<kFp8>::kStages * kWarps * 16 : 0);
+  static constexpr uint32_t kScan = kBar + 2 * Shape<kFp8>::kStages * 8;  // 5 + 5 warp sums, slot
+  static constexpr uint32_t kMisc = kScan + 2 * 5 * 8 + 16;
+  static constexpr uint32_t kBytes = kMisc + 16 + 1024;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8x8 matrix of 16-bit elements held one row pair per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four e4m3 codes to two f16x2 words (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+// Length of sequence b, clamped to the table; one outside it is reported.
+__device__ __forceinline__ int length_of(const PagedAttentionArgs& a, int b) {
+  int len = __ldg(a.len + b);
+  if (len < 0 || len > a.max_len) {
+    atomicOr(a.err, kErrLength);
+    len = len < 0 ? 0 : a.max_len;
+  }
+  return len;
+}
+
+template <int NT>
+__device__ __forceinline__ int row_tiles(const PagedAttentionArgs& a, int row) {
+  const int b = row / a.groups;
+  int lo, hi;
+  paged_row_range(length_of(a, b), a.n, (row - b * a.groups) * NT, NT, a.window, &lo, &hi);
+  return paged_row_tiles(lo, hi);
+}
+
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// Finds chunk `cid` of the call. Chunks are counted in the low half of the scanned
+// words and those of rows with several in the high half.
+template <int NT>
+__device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid, uint64_t* sums,
+                                           ScanSlot* slot) {
+  const int t = static_cast<int>(threadIdx.x);
+  const int warp = t >> 5, lane = t & 31;
+  const int per = (a.rows + kThreads - 1) / kThreads;
+  const int r0 = min(a.rows, t * per), r1 = min(a.rows, r0 + per);
+  if (t == 0) slot->row = -1;
+  int first = 0;
+  uint64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    first = row_tiles<NT>(a, r);
+    mine += static_cast<uint64_t>(first);
+  }
+  uint64_t inc = warp_scan(mine, lane);
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  uint64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps + 1; ++w) total += sums[w];
+  const int chunk = paged_chunk_tiles(static_cast<int64_t>(total), a.target);
+
+  mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const uint64_t n = paged_row_chunks(per == 1 ? first : row_tiles<NT>(a, r), chunk);
+    mine += n | (n > 1 ? n << 32 : 0);
+  }
+  inc = warp_scan(mine, lane);
+  if (lane == 31) sums[kWarps + 1 + warp] = inc;
+  __syncthreads();
+  uint64_t at = inc - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) at += sums[kWarps + 1 + w];
+  if (static_cast<uint32_t>(cid) - static_cast<uint32_t>(at) < static_cast<uint32_t>(mine)) {
+    for (int r = r0; r < r1; ++r) {
+      const int n = paged_row_chunks(per == 1 ? first : row_tiles<NT>(a, r), chunk);
+      const int i = cid - static_cast<int>(static_cast<uint32_t>(at));
+      if (i < n) {
+        slot->row = r;
+        slot->split = i;
+        slot->chunks = n;
+        slot->part = static_cast<int>(at >> 32);
+        break;
+      }
+      at += static_cast<uint64_t>(n) | (n > 1 ? static_cast<uint64_t>(n) << 32 : 0);
+    }
+  }
+  __syncthreads();
+  return slot->row >= 0;
+}
+
+template <bool kFp8, int NT>
+__global__ void __launch_bounds__(kThreads)
+    paged_attention_kernel(const __grid_constant__ PagedMaps maps, const PagedAttentionArgs a) {
+  using L = Smem<kFp8, NT>;
+  constexpr int kStages = Shape<kFp8>::kStages;
+  constexpr uint32_t kTileBytes = Shape<kFp8>::kTileBytes;
+  constexpr uint32_t kRowBytes = kHeadDim * Shape<kFp8>::kElem;
+  griddep_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
+  auto full_bar = [&](int s) { return sbase + L::kBar + 8u * s; };
+  auto empty_bar = [&](int s) { return sbase + L::kBar + 8u * (kStages + s); };
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int g = static_cast<int>(blockIdx.x % kNumKvHeads);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), kWarps);
+    }
+    fence_barrier_init();
+  }
+  // The tokens, lengths and pages, and the workspace, may still be in use by
+  // the kernel before.
+  griddep_wait();
+  if (threadIdx.x == 0)
+    *abort_flag = (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) ? 1 : 0;
+  ScanSlot* slot = reinterpret_cast<ScanSlot*>(smem + L::kScan + 2 * 5 * 8);
+  if (!find_chunk<NT>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
+                      reinterpret_cast<uint64_t*>(smem + L::kScan), slot))
+    return;  // past the call's last chunk
+  const bool skip = *abort_flag != 0;
+  const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
+  if (slot->split == 0 && g == 0 && threadIdx.x == 0) a.meta[row] = make_int2(slot->part, chunks);
+  const int b = row / a.groups;
+  const int t0 = (row - b * a.groups) * NT;
+  const int len = min(max(__ldg(a.len + b), 0), a.max_len);
+  const int idx0 = len - a.n + t0;  // index of the row's first token
+  int lo, hi, tile_a, tile_b;
+  paged_row_range(len, a.n, t0, NT, a.window, &lo, &hi);
+  paged_chunk_range(paged_row_tiles(lo, hi), chunks, slot->split, &tile_a, &tile_b);
+  const int key_a = (lo / kPagedTile + tile_a) * kPagedTile;  // first key of the chunk's tiles
+  const int n_tiles = tile_b - tile_a;
+  const int page_log2 = a.cache.page_log2;
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer
+    if (!skip && n_tiles > 0) {
+      if (lane == 0) {
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+      }
+      const int P = 1 << page_log2;
+      const int box = P < kPagedTile ? P : kPagedTile;  // keys per copy
+      const int boxes = kPagedTile / box;
+      const int last_page = (hi - 1) >> page_log2;
+      const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+      // Lane i holds page number pbase + i of the sequence, and its scales; the
+      // next 32 are loaded while these are used. Pages before the first visible
+      // key or past the last are not looked at: their entries may be unset.
+      struct Entry {
+        int page;
+        float ks, vs;
+      };
+      auto fetch = [&](int pi) {
+        Entry e = {a.cache.num_pages, 1.f, 1.f};
+        if (pi <= last_page && pi >= (lo >> page_log2)) {
+          const int page = __ldg(table + pi);
+          if (paged_page_ok(page, a.cache.num_pages)) {
+            e.page = page;
+            if (kFp8) {
+              e.ks = __ldg(a.cache.k_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
+              e.vs = __ldg(a.cache.v_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
+            }
+          } else {
+            // out of the map's range: the copy fills zeros
+            atomicOr(a.err, kErrPage);
+          }
+        }
+        return e;
+      };
+      int pbase = key_a >> page_log2;
+      Entry cur = fetch(pbase + lane), nxt = fetch(pbase + 32 + lane);
+      int issued = 0;
+      for (int i = 0; i < n_tiles; ++i) {
+        const int s = i % kStages;
+        const int key0 = key_a + i * kPagedTile;
+        if ((key0 >> page_log2) >= pbase + 32) {
+          pbase += 32;
+          cur = nxt;
+          nxt = fetch(pbase + 32 + lane);
+        }
+        if (i >= kStages && !mbar_wait_warp(empty_bar(s), ((i / kStages) - 1) & 1, abort_flag,
+                                            a.err, kErrTimeout, kWaitTimeoutNs))
+          break;
+        // pages of this tile that hold a visible key
+        const int key = key0 + (lane & 3) * box;
+        const int pg = key >> page_log2;
+        const int page = __shfl_sync(0xffffffffu, cur.page, (pg - pbase) & 31);
+        const bool load = (lane & 3) < boxes && key < hi && key + box > lo;
+        const int n_load = __popc(__ballot_sync(0xffffffffu, load) & 0xFu);
+        if (kFp8) {
+          const int pw = (key0 + (lane & 3) * 16) >> page_log2;  // page of warp's 16 keys
+          const float ks = __shfl_sync(0xffffffffu, cur.ks, (pw - pbase) & 31);
+          const float vs = fmaxf(__shfl_sync(0xffffffffu, cur.vs, (pw - pbase) & 31), 0x1p-100f);
+          if (lane < 4)
+            *reinterpret_cast<float4*>(smem + L::kPage + (s * kWarps + lane) * 16) =
+                make_float4(ks * kScaleLog2, log2f(vs), 1.f / vs, 0.f);
+          __syncwarp();
+        }
+        if (lane == 0)
+          mbar_arrive_expect_tx(full_bar(s),
+                                2u * static_cast<uint32_t>(n_load * box) * kRowBytes);
+        __syncwarp();
+        if (load && lane < 8) {
+          const uint32_t dst = sbase + (lane < 4 ? L::kK : L::kV) + s * kTileBytes +
+                               static_cast<uint32_t>((lane & 3) * box) * kRowBytes;
+          tma_load_4d(dst, lane < 4 ? &maps.k : &maps.v, full_bar(s), 0, g, key & (P - 1), page);
+        }
+        issued = i + 1;
+      }
+      __syncwarp();
+      if (*abort_flag) {
+        volatile int never = 0;
+        for (int i = max(0, issued - kStages); i < issued; ++i)
+          mbar_wait(full_bar(i % kStages), (i / kStages) & 1, &never, nullptr, 0, kWaitTimeoutNs);
+      }
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int t = static_cast<int>(threadIdx.x);  // 0..127
+  // The row's queries, rotated, as the B operand's 16-bit terms. Sixteen threads
+  // take a head: thread e elements 4e .. 4e+3.
+  {
+    const int hh = t >> 4, d0 = (t & 15) * 4;
+#pragma unroll
+    for (int tk = 0; tk < NT; ++tk) {
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+      if (t0 + tk < a.n && idx0 + tk >= 0) {
+        int p = a.pos ? __ldg(a.pos + static_cast<int64_t>(b) * a.n + t0 + tk) : idx0 + tk;
+        if (p < 0 || p >= kMaxPosition) {
+          atomicOr(a.err, kErrPosition);
+          p = p < 0 ? 0 : kMaxPosition - 1;
+        }
+        const uint16_t* q = a.q + b * a.q_batch + (t0 + tk) * a.q_token +
+                            (g * kGroup + hh) * kHeadDim;
+        const uint2 own = __ldg(reinterpret_cast<const uint2*>(q + d0));
+        const uint2 other = __ldg(reinterpret_cast<const uint2*>(q + (d0 ^ 32)));
+        const float4* cs = reinterpret_cast<const float4*>(
+            a.rope + static_cast<int64_t>(p) * kRopePairs + (d0 & 31));
+        const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
+        const float x[4] = {bf16lo_to_f32(own.x), bf16hi_to_f32(own.x), bf16lo_to_f32(own.y),
+                            bf16hi_to_f32(own.y)};
+        const float z[4] = {bf16lo_to_f32(other.x), bf16hi_to_f32(other.x),
+                            bf16lo_to_f32(other.y), bf16hi_to_f32(other.y)};
+        const float cc[4] = {c0.x, c0.z, c1.x, c1.z}, ss[4] = {c0.y, c0.w, c1.y, c1.w};
+        const float sign = d0 < 32 ? -1.f : 1.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = fmaf(x[e], cc[e], sign * z[e] * ss[e]);
+      }
+      const uint32_t at = L::kQ + static_cast<uint32_t>((tk * kGroup + hh) * kHeadDim + d0) * 2;
+      if (kFp8) {
+        // largest element to [1, 2): f16 then holds the others to 2^-12 of themselves
+        // or 2^-25 of the largest
+        float top = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+#pragma unroll
+        for (int d = 8; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        e = max(-100, min(e, 100));
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if (d0 == 0)
+          *reinterpret_cast<float*>(smem + L::kQExp + (tk * kGroup + hh) * 4) =
+              __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        *reinterpret_cast<uint2*>(smem + at) =
+            make_uint2(pack_f16x2(y[0] * f, y[1] * f), pack_f16x2(y[2] * f, y[3] * f));
+      } else {
+        const uint32_t h0 = pack_bf16x2(y[0], y[1]), h1 = pack_bf16x2(y[2], y[3]);
+        *reinterpret_cast<uint2*>(smem + at) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(smem + at + NT * kGroup * kHeadDim * 2) =
+            make_uint2(pack_bf16x2(y[0] - bf16lo_to_f32(h0), y[1] - bf16hi_to_f32(h0)),
+                       pack_bf16x2(y[2] - bf16lo_to_f32(h1), y[3] - bf16hi_to_f32(h1)));
+      }
+    }
+  }
+  named_barrier(1, kWarps * 32);
+
+  const int gr = lane >> 2, tc = lane & 3;
+  // B fragments of Q^T: column gr = head, rows 2tc, 2tc+1 and 2tc+8, 2tc+9 of k step kk.
+  // e4m3: a lane's 16 bytes of a key are elements 16tc .. 16tc+15, four per k step, so
+  // those rows stand for elements 16tc+4kk .. 16tc+4kk+3 (any order of the 64 will do).
+  uint32_t qh[NT][4][2], ql[kFp8 ? 1 : NT][4][2];
+  float qs[kFp8 ? NT : 1][2];
+#pragma unroll
+  for (int tk = 0; tk < NT; ++tk) {
+    const uint8_t* q = smem + L::kQ + (tk * kGroup + gr) * kHeadDim * 2;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int d0 = kFp8 ? 16 * tc + 4 * kk : 16 * kk + 2 * tc;
+      const int d1 = kFp8 ? d0 + 2 : d0 + 8;
+      qh[tk][kk][0] = *reinterpret_cast<const uint32_t*>(q + d0 * 2);
+      qh[tk][kk][1] = *reinterpret_cast<const uint32_t*>(q + d1 * 2);
+      if (!kFp8) {
+        const uint8_t* q2 = q + NT * kGroup * kHeadDim * 2;
+        ql[kFp8 ? 0 : tk][kk][0] = *reinterpret_cast<const uint32_t*>(q2 + d0 * 2);
+        ql[kFp8 ? 0 : tk][kk][1] = *reinterpret_cast<const uint32_t*>(q2 + d1 * 2);
+      }
+    }
+    if (kFp8) {
+      const float2 e = *reinterpret_cast<const float2*>(smem + L::kQExp + (tk * kGroup + 2 * tc) * 4);
+      qs[kFp8 ? tk : 0][0] = e.x;
+      qs[kFp8 ? tk : 0][1] = e.y;
+    }
+  }
+
+  // O^T of this warp's keys: four tiles of 16 head_dim rows; columns 2tc, 2tc+1 (heads).
+  float o[NT][4][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int tk = 0; tk < NT; ++tk) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[tk][i][0] = o[tk][i][1] = o[tk][i][2] = o[tk][i][3] = 0.f;
+    m[tk][0] = m[tk][1] = kNoMax;
+    l[tk][0] = l[tk][1] = 0.f;
+  }
+  // Keys that every token of the row sees need no mask.
+  const int all_hi = idx0 + 1;  // keys below it are not past the first token
+  const int all_lo = a.window > 0 ? min(idx0 + NT, len) - a.window : 0;
+  bool ok = !skip;
+  for (int i = 0; ok && i < n_tiles; ++i) {
+    const int s = i % kStages;
+    if (!(ok = mbar_wait_warp(full_bar(s), (i / kStages) & 1, abort_flag, a.err, kErrTimeout,
+                              kWaitTimeoutNs)))
+      break;
+    const uint32_t sk = sbase + L::kK + s * kTileBytes + 16 * warp * kRowBytes;
+    const uint32_t sv = sbase + L::kV + s * kTileBytes + 16 * warp * kRowBytes;
+    const int key0 = key_a + i * kPagedTile + 16 * warp;
+    float4 pagef = make_float4(kScaleLog2, 0.f, 1.f, 0.f);
+    if (kFp8) pagef = *reinterpret_cast<const float4*>(smem + L::kPage + (s * kWarps + warp) * 16);
+
+    // S^T: rows = keys gr and gr+8, columns = heads 2tc and 2tc+1
+    float sc[NT][4];
+#pragma unroll
+    for (int tk = 0; tk < NT; ++tk) sc[tk][0] = sc[tk][1] = sc[tk][2] = sc[tk][3] = 0.f;
+    if (kFp8) {
+      const uint4 ka = lds128(sk + gr * 64 + ((tc ^ ((gr >> 1) & 3)) << 4));
+      const uint4 kb = lds128(sk + (gr + 8) * 64 + ((tc ^ ((gr >> 1) & 3)) << 4));
+      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t f[4];
+        e4m3x4_to_f16(wa[kk], f[0], f[2]);
+        e4m3x4_to_f16(wb[kk], f[1], f[3]);
+#pragma unroll
+        for (int tk = 0; tk < NT; ++tk) mma_f16(sc[tk], f, qh[tk][kk][0], qh[tk][kk][1]);
+      }
+    } else {
+      const int r = (lane & 7) + 8 * ((lane >> 3) & 1);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t f[4];
+        ldsm_x4(sk + r * 128 + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+#pragma unroll
+        for (int tk = 0; tk < NT; ++tk) {
+          mma_bf16(sc[tk], f, qh[tk][kk][0], qh[tk][kk][1]);
+          mma_bf16(sc[tk], f, ql[kFp8 ? 0 : tk][kk][0], ql[kFp8 ? 0 : tk][kk][1]);
+        }
+      }
+    }
+
+    // Exponents x - m in log2 units; masked keys -inf.
+    const bool edge = key0 + 16 > all_hi || key0 < all_lo;
+    bool above = false;
+    float d[NT][4];
+#pragma unroll
+    for (int tk = 0; tk < NT; ++tk) {
+      const float c0 = kFp8 ? pagef.x * qs[kFp8 ? tk : 0][0] : kScaleLog2;
+      const float c1 = kFp8 ? pagef.x * qs[kFp8 ? tk : 0][1] : kScaleLog2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        d[tk][e] = fmaf(sc[tk][e], e & 1 ? c1 : c0, pagef.y - m[tk][e & 1]);
+      if (edge) {
+        const int top = idx0 + tk, k0 = key0 + gr, k1 = k0 + 8;
+        const int low = a.window > 0 ? top - a.window : -1;
+        if (k0 > top || k0 <= low) d[tk][0] = d[tk][1] = -INFINITY;
+        if (k1 > top || k1 <= low) d[tk][2] = d[tk][3] = -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) above = above || d[tk][e] > kRescaleThreshold;
+    }
+    if (__any_sync(0xffffffffu, above)) {
+      // new maxima of every head, over the warp's 16 keys
+#pragma unroll
+      for (int tk = 0; tk < NT; ++tk) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float c = kFp8 ? pagef.x * qs[kFp8 ? tk : 0][h] : kScaleLog2;
+          const float x0 = d[tk][h] == -INFINITY ? kNoMax : fmaf(sc[tk][h], c, pagef.y);
+          const float x1 = d[tk][2 + h] == -INFINITY ? kNoMax : fmaf(sc[tk][2 + h], c, pagef.y);
+          float mx = fmaxf(m[tk][h], fmaxf(x0, x1));
+#pragma unroll
+          for (int w = 4; w < 32; w *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          const float alpha = ex2_approx(m[tk][h] - mx);
+          m[tk][h] = mx;
+          l[tk][h] *= alpha;
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            o[tk][mt][h] *= alpha;
+            o[tk][mt][2 + h] *= alpha;
+          }
+          if (d[tk][h] != -INFINITY) d[tk][h] = x0 - mx;
+          if (d[tk][2 + h] != -INFINITY) d[tk][2 + h] = x1 - mx;
+        }
+      }
+    }
+
+    // P^T, transposed to the B operand (row = key, column = head)
+    uint32_t ph[NT][2], pl[kFp8 ? 1 : NT][2];
+#pragma unroll
+    for (int tk = 0; tk < NT; ++tk) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = ex2_approx(d[tk][e]);
+      l[tk][0] = fmaf(p[0] + p[2], pagef.z, l[tk][0]);
+      l[tk][1] = fmaf(p[1] + p[3], pagef.z, l[tk][1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (kFp8) {
+          ph[tk][h] = transpose8(pack_f16x2(p[2 * h], p[2 * h + 1]));
+        } else {
+          const uint32_t w = pack_bf16x2(p[2 * h], p[2 * h + 1]);
+          ph[tk][h] = transpose8(w);
+          pl[kFp8 ? 0 : tk][h] = transpose8(
+              pack_bf16x2(p[2 * h] - bf16lo_to_f32(w), p[2 * h + 1] - bf16hi_to_f32(w)));
+        }
+      }
+    }
+
+    // O^T += V^T P^T. On an edge the values of a token's masked keys are zeroed:
+    // their p is 0, but what lies there may be infinite or NaN.
+    auto accumulate = [&](int mt, const uint32_t (&f)[4]) {
+#pragma unroll
+      for (int tk = 0; tk < NT; ++tk) {
+        if (edge) {
+          const int top = idx0 + tk, low = a.window > 0 ? top - a.window : -1;
+          uint32_t z[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k0 = key0 + 8 * h + 2 * tc;
+            const uint32_t keep = (k0 <= top && k0 > low ? 0x0000FFFFu : 0u) |
+                                  (k0 + 1 <= top && k0 + 1 > low ? 0xFFFF0000u : 0u);
+            z[2 * h] = f[2 * h] & keep;
+            z[2 * h + 1] = f[2 * h + 1] & keep;
+          }
+          if (kFp8) {
+            mma_f16(o[tk][mt], z, ph[tk][0], ph[tk][1]);
+          } else {
+            mma_bf16(o[tk][mt], z, ph[tk][0], ph[tk][1]);
+            mma_bf16(o[tk][mt], z, pl[kFp8 ? 0 : tk][0], pl[kFp8 ? 0 : tk][1]);
+          }
+        } else if (kFp8) {
+          mma_f16(o[tk][mt], f, ph[tk][0], ph[tk][1]);
+        } else {
+          mma_bf16(o[tk][mt], f, ph[tk][0], ph[tk][1]);
+          mma_bf16(o[tk][mt], f, pl[kFp8 ? 0 : tk][0], pl[kFp8 ? 0 : tk][1]);
+        }
+      }
+    };
+    if (kFp8) {
+      // a lane's word: keys 2tc, 2tc+1 of elements 16c+2gr, 16c+2gr+1; rows gr and
+      // gr+8 of tile c stand for those two
+      const int r = (lane & 7) + 8 * ((lane >> 3) & 1);
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t w[4];
+        ldsm_x4_trans(sv + r * 64 + (((c + (lane >> 4)) ^ ((r >> 1) & 3)) << 4), w[0], w[1], w[2],
+                      w[3]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t f[4];
+          e4m3x4_to_f16(__byte_perm(w[2 * u], 0, 0x3120), f[0], f[1]);
+          e4m3x4_to_f16(__byte_perm(w[2 * u + 1], 0, 0x3120), f[2], f[3]);
+          accumulate(c + u, f);
+        }
+      }
+    } else {
+      const int r = (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        uint32_t f[4];
+        ldsm_x4_trans(sv + r * 128 + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4), f[0], f[1],
+                      f[2], f[3]);
+        accumulate(mt, f);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty_bar(s));
+  }
+
+  // ---- join the warps
+  named_barrier(1, kWarps * 32);  // every warp has done with the tiles
+  float* mo = reinterpret_cast<float*>(smem + L::kMerge + warp * L::kMergeWarp);
+#pragma unroll
+  for (int tk = 0; tk < NT; ++tk)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float* row_o = mo + (tk * kGroup + 2 * tc + h) * kHeadDim;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        row_o[16 * mt + (kFp8 ? 2 * gr : gr)] = o[tk][mt][h];
+        row_o[16 * mt + (kFp8 ? 2 * gr + 1 : gr + 8)] = o[tk][mt][2 + h];
+      }
+      float sum = l[tk][h];
+#pragma unroll
+      for (int w = 4; w < 32; w *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      if (gr == 0) {
+        float* ml = mo + NT * kGroup * kHeadDim;
+        ml[tk * kGroup + 2 * tc + h] = m[tk][h];
+        ml[NT * kGroup + tk * kGroup + 2 * tc + h] = sum;
+      }
+    }
+  named_barrier(1, kWarps * 32);
+  if (skip || *abort_flag) return;
+  const int hh = t >> 4, d0 = (t & 15) * 4;
+#pragma unroll
+  for (int tk = 0; tk < NT; ++tk) {
+    if (t0 + tk >= a.n) break;
+    const int r = tk * kGroup + hh;
+    float mw[kWarps], M = kNoMax;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float* base = reinterpret_cast<const float*>(smem + L::kMerge + w * L::kMergeWarp);
+      mw[w] = base[NT * kGroup * kHeadDim + r];
+      M = fmaxf(M, mw[w]);
+    }
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float* base = reinterpret_cast<const float*>(smem + L::kMerge + w * L::kMergeWarp);
+      const float f = ex2_approx(mw[w] - M);
+      sum = fmaf(f, base[NT * kGroup * (kHeadDim + 1) + r], sum);
+      const float4 v = *reinterpret_cast<const float4*>(base + r * kHeadDim + d0);
+      acc[0] = fmaf(f, v.x, acc[0]);
+      acc[1] = fmaf(f, v.y, acc[1]);
+      acc[2] = fmaf(f, v.z, acc[2]);
+      acc[3] = fmaf(f, v.w, acc[3]);
+    }
+    if (chunks == 1) {
+      const float sink = __ldg(a.sinks + g * kGroup + hh) * kLog2e;
+      const float Mf = fmaxf(sink, M);
+      const float f = ex2_approx(M - Mf);
+      const float den = fmaf(f, sum, ex2_approx(sink - Mf));
+      const float scale = M > kNoMax ? f / den : 0.f;
+      *reinterpret_cast<uint2*>(
+          a.out + ((static_cast<int64_t>(b) * a.n + t0 + tk) * kNumHeads + g * kGroup + hh) *
+                      kHeadDim + d0) =
+          make_uint2(pack_bf16x2(acc[0] * scale, acc[1] * scale),
+                     pack_bf16x2(acc[2] * scale, acc[3] * scale));
+    } else {
+      const int64_t pr = (static_cast<int64_t>(part) * kNumKvHeads + g) * (NT * kGroup) + r;
+      *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + d0) =
+          make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (d0 == 0) a.part_ml[pr] = make_float2(M, sum);
+    }
+  }
+}
+
+// Joins the chunks of the rows that have several, with the sink, normalises and
+// rounds: `warps` warps of a CTA per output row (token and head), each over every
+// warps-th chunk, two elements a lane.
+template <int NT>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttentionArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float2 part[8][32];
+  __shared__ float2 part_ml[8];
+  const int warps = static_cast<int>(blockDim.x >> 5);
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int row = static_cast<int>(blockIdx.x), r = static_cast<int>(blockIdx.y);  // r: tk, head
+  const int tk = r / kNumHeads, h = r % kNumHeads;
+  if (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) return;
+  const int2 meta = a.meta[row];
+  const int b = row / a.groups, t = (row - b * a.groups) * NT + tk;
+  if (meta.y == 1 || t >= a.n) return;
+  const int64_t stride = kNumKvHeads * NT * kGroup;
+  const int64_t first = meta.x * stride + (h / kGroup) * (NT * kGroup) + tk * kGroup + h % kGroup;
+  float M = kNoMax, sum = 0.f, o0 = 0.f, o1 = 0.f;
+  constexpr int kBatch = 8;
+  for (int s0 = warp; s0 < meta.y; s0 += kBatch * warps) {
+    float2 ml[kBatch], v[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int s = s0 + j * warps;
+      ml[j] = make_float2(kNoMax, 0.f);
+      v[j] = make_float2(0.f, 0.f);
+      if (s < meta.y) {
+        ml[j] = a.part_ml[first + s * stride];
+        v[j] = *reinterpret_cast<const float2*>(a.part_o + (first + s * stride) * kHeadDim +
+                                                2 * lane);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) top = fmaxf(top, ml[j].x);
+    const float f = ex2_approx(M - top);
+    M = top;
+    sum *= f;
+    o0 *= f;
+    o1 *= f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float fj = ex2_approx(ml[j].x - top);
+      sum = fmaf(fj, ml[j].y, sum);
+      o0 = fmaf(fj, v[j].x, o0);
+      o1 = fmaf(fj, v[j].y, o1);
+    }
+  }
+  part[warp][lane] = make_float2(o0, o1);
+  if (lane == 0) part_ml[warp] = make_float2(M, sum);
+  __syncthreads();
+  if (warp > 0) return;
+  const float sink = __ldg(a.sinks + h) * kLog2e;
+  float Mf = sink;
+  for (int w = 0; w < warps; ++w) Mf = fmaxf(Mf, part_ml[w].x);
+  float den = ex2_approx(sink - Mf);
+  o0 = o1 = 0.f;
+  for (int w = 0; w < warps; ++w) {
+    const float f = ex2_approx(part_ml[w].x - Mf);
+    den = fmaf(f, part_ml[w].y, den);
+    o0 = fmaf(f, part[w][lane].x, o0);
+    o1 = fmaf(f, part[w][lane].y, o1);
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  reinterpret_cast<uint32_t*>(a.out + ((static_cast<int64_t>(b) * a.n + t) * kNumHeads + h) *
+                                          kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
+}
+
+template <bool kFp8, int NT>
+cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStream_t stream) {
+  using L = Smem<kFp8, NT>;
+  cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<kFp8, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(L::kBytes));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  // no more chunks than the visible keys can give
+  const int most = paged_row_tiles(0, a.window > 0 && a.window + NT < a.max_len
+                                          ? a.window + NT + kPagedTile : a.max_len);
+  int64_t chunks = paged_max_chunks(a.rows, a.target);
+  if (static_cast<int64_t>(a.rows) * most < chunks) chunks = static_cast<int64_t>(a.rows) * most;
+  cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  e = cudaLaunchKernelEx(&cfg, paged_attention_kernel<kFp8, NT>, maps, a);
+  if (e != cudaSuccess || most == 1) return e;
+  // few output rows: several warps each, since their chunks are many
+  const int warps = static_cast<int64_t>(a.rows) * NT * kNumHeads <= 148 * 8 ? 8 : 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows), NT * kNumHeads);
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT>, a);
+}
+
+}  // namespace
+
+int paged_row_tokens(int n) { return n == 1 ? 1 : n == 2 ? 2 : 4; }
+
+// About four waves of three CTAs per SM, eight (one per kv head) to a chunk.
+int paged_target(int n) {
+  (void)n;
+  return 148 * 3 * 4 / kNumKvHeads;
+}
+
+size_t paged_workspace_bytes(int64_t rows, int n, size_t off[3]) {
+  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(n))) * kNumKvHeads *
+                       paged_row_tokens(n) * kGroup;
+  off[0] = 0;
+  off[1] = parts * kHeadDim * sizeof(float);
+  off[2] = off[1] + parts * sizeof(float2);
+  return off[2] + ((static_cast<size_t>(rows) * sizeof(int2) + 15) & ~static_cast<size_t>(15));
+}
+
+cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& a,
+                                   cudaStream_t stream) {
+  if (a.cache.fp8) {
+    if (a.n == 1) return launch<true, 1>(maps, a, stream);
+    if (a.n == 2) return launch<true, 2>(maps, a, stream);
+    return launch<true, 4>(maps, a, stream);
+  }
+  if (a.n == 1) return launch<false, 1>(maps, a, stream);
+  if (a.n == 2) return launch<false, 2>(maps, a, stream);
+  return launch<false, 4>(maps, a, stream);
+}
+
+}  // namespace gqa

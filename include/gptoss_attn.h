@@ -70,7 +70,8 @@ enum gptoss_attn_status {
   GPTOSS_ATTN_ERR_ALLOC = -8,           /* library-owned device memory could not be allocated */
   GPTOSS_ATTN_ERR_DEVICE_TIMEOUT = -9,  /* a kernel pipeline wait ran out (reported by check) */
   GPTOSS_ATTN_ERR_BAD_POSITION = -10,   /* a position was outside [0, 131072) (reported by check) */
-  GPTOSS_ATTN_ERR_BAD_LENGTH = -11      /* a decode length was outside [0, max_len] (reported by check) */
+  GPTOSS_ATTN_ERR_BAD_LENGTH = -11,     /* a decode length was outside [0, max_len] (reported by check) */
+  GPTOSS_ATTN_ERR_BAD_PAGE = -12        /* a page number was outside [0, num_pages) (reported by check) */
 };
 
 /* ABI version of the loaded library (GPTOSS_ATTN_ABI_VERSION). */
@@ -309,6 +310,125 @@ int gptoss_attn_decode_noalloc(const void* q, const void* kcache, const void* vc
                                int batch, int max_len, cudaStream_t stream);
 
 /*
+ * Paged key/value cache: a pool of pages, each holding page_size consecutive
+ * tokens of one sequence, found through a table of page numbers. The gpt-oss
+ * pages name a cache (use_cache in the configuration table) but no layout;
+ * these calls serve sequences that grow without one contiguous buffer each,
+ * and hold the cache in 8 bits where asked to.
+ *
+ * Element d of kv head h of token t of page p lies at
+ *   p * page_stride + t * token_stride + h * head_stride + d
+ * (strides in elements, multiples of 16 bytes; K and V share them), so pages may
+ * be laid out by token or by head, or be views of a larger buffer.
+ *
+ * GPTOSS_ATTN_PAGES_BF16: bf16 values; the scales are NULL.
+ * GPTOSS_ATTN_PAGES_E4M3: e4m3 codes (4 exponent, 3 mantissa bits, no infinity);
+ *   the value is code * scale[p][h], with fp32 scales [num_pages][8] for K and for
+ *   V. The append writes powers of two; attention takes any positive finite scale.
+ */
+enum gptoss_attn_pages { GPTOSS_ATTN_PAGES_BF16 = 0, GPTOSS_ATTN_PAGES_E4M3 = 1 };
+
+typedef struct gptoss_attn_paged_cache {
+  void* k;               /* 16-byte aligned */
+  void* v;
+  float* k_scale;        /* [num_pages][8]; E4M3 only, else NULL */
+  float* v_scale;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t num_pages;     /* >= 1 */
+  int32_t page_size;     /* tokens per page: 16, 32, 64 or 128 */
+  int32_t type;          /* gptoss_attn_pages */
+} gptoss_attn_paged_cache;
+
+/*
+ * Appends the newest tokens of each sequence: token t < count[b] of sequence b has
+ * index i = len[b] - count[b] + t and goes to page table[b][i / page_size], slot
+ * i % page_size; the key is rotated at pos[b][t] on the way.
+ *   k, v    bf16 [batch][n][8][64], not rotated; heads and elements contiguous, the
+ *           other strides given in elements (multiples of 8), so slices of a
+ *           fused projection are taken as they are
+ *   pos     int32 [batch][n], in [0, 131072)
+ *   table   int32 [batch][max_pages]; max_pages * page_size <= 131072. Only the
+ *           entries of pages that take new tokens are read
+ *   len     int32 [batch], tokens of each sequence with the new ones
+ *   count   int32 [batch], 0 <= count[b] <= n, or NULL: n for every sequence; rows
+ *           of k, v and pos past count[b] are not used
+ * bf16 pages hold exactly what gptoss_attn_prefill_chunk() would write. e4m3 pages:
+ * per (page, head), the scale is the least power of two 2^e, -64 <= e <= 120, with
+ * every new finite |value| <= 448 * 2^e, or the scale that the page has, if it holds
+ * earlier tokens of the sequence and that is larger; if it is smaller, the
+ * codes of those tokens are moved to the new scale (exact but for values that
+ * become subnormal). Infinities saturate; NaN stays NaN. A page that gets its
+ * slot 0 in this call forgets the scale that it had. A page that two sequences
+ * share must not take new tokens. Slots at or past len[b] are left as they are.
+ * A sequence with count[b] outside [0, n] or len[b] outside [count[b],
+ * max_pages * page_size] gets nothing (reported by check as BAD_LENGTH); a page
+ * number outside [0, num_pages) is skipped (BAD_PAGE). One kernel on `stream`.
+ * batch, n >= 1; batch <= 65535; n <= 131072.
+ */
+int gptoss_attn_paged_append(const gptoss_attn_paged_cache* cache, const void* k, const void* v,
+                             int64_t k_batch_stride, int64_t k_token_stride,
+                             int64_t v_batch_stride, int64_t v_token_stride, const int32_t* pos,
+                             const int32_t* table, const int32_t* len, const int32_t* count,
+                             int batch, int n, int max_pages, cudaStream_t stream);
+
+/* gptoss_attn_paged_append() with the YaRN rotation (see gptoss_attn_init_yarn). */
+int gptoss_attn_paged_append_yarn(const gptoss_attn_paged_cache* cache, const void* k,
+                                  const void* v, int64_t k_batch_stride, int64_t k_token_stride,
+                                  int64_t v_batch_stride, int64_t v_token_stride,
+                                  const int32_t* pos, const int32_t* table, const int32_t* len,
+                                  const int32_t* count, int batch, int n, int max_pages,
+                                  cudaStream_t stream);
+
+/*
+ * Bytes of device workspace gptoss_attn_paged_attention() needs; it does not
+ * depend on the capacity of the cache. Returns 0 for invalid sizes.
+ */
+size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n);
+
+/*
+ * Attention of the n newest tokens of each sequence over its pages (n = 1: a decode
+ * step; n > 1: drafted tokens, or a piece of a prompt on a cached prefix). Their keys
+ * and values are in the pages already. Token t has index i = len[b] - n + t and sees
+ * keys j <= i (and, for W > 0, j > i - W); one with a negative index sees nothing
+ * and gives zeros.
+ *   q       bf16 [batch][n][64][64], not rotated; heads and elements contiguous, the
+ *           other strides given in elements (multiples of 8)
+ *   pos     int32 [batch][n] rotary positions, or NULL: the tokens' indices
+ *   table   int32 [batch][max_pages]; entries of pages that hold no visible key
+ *           are not read, and so may be unset
+ *   len     int32 [batch], 0 <= len[b] <= max_pages * page_size (others are clamped
+ *           and reported by check as BAD_LENGTH)
+ *   sinks   fp32 [64]; -inf allowed
+ *   out     bf16 [batch][n][64][64], contiguous
+ *   workspace of gptoss_attn_paged_attention_workspace_bytes(batch, n) bytes, 16-byte
+ *           aligned, uninitialised; calls that overlap in time need separate ones
+ * A page number outside [0, num_pages) is reported by check (BAD_PAGE) and read as
+ * a page of zeros. What lies in slots that no token sees (later tokens' rows,
+ * stale rows, NaN) does not reach the output. Scores, softmax and sums are fp32;
+ * rotated q and the probabilities keep 16 (bf16 pages) or 11 bits (e4m3 pages).
+ * batch >= 1, n >= 1, batch * n <= 131072. One or two kernels on `stream`. How the work
+ * is cut depends on the lengths of the whole batch, and the order of the fp32 sums
+ * with it.
+ */
+int gptoss_attn_paged_attention(const gptoss_attn_paged_cache* cache, const void* q,
+                                int64_t q_batch_stride, int64_t q_token_stride,
+                                const int32_t* pos, const int32_t* table, const float* sinks,
+                                const int32_t* len, int window, void* out, int batch, int n,
+                                int max_pages, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/* gptoss_attn_paged_attention() with queries rotated by YaRN; the pages must
+ * hold YaRN-rotated keys. */
+int gptoss_attn_paged_attention_yarn(const gptoss_attn_paged_cache* cache, const void* q,
+                                     int64_t q_batch_stride, int64_t q_token_stride,
+                                     const int32_t* pos, const int32_t* table, const float* sinks,
+                                     const int32_t* len, int window, void* out, int batch, int n,
+                                     int max_pages, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+/*
  * Diagnostic, with no counterpart on the gpt-oss pages: exercises the failure
  * path every kernel pipeline wait uses. One thread waits, through the same
  * bounded wait, on a barrier that nothing arrives at; after timeout_us
@@ -325,7 +445,7 @@ int gptoss_attn_debug_wait_timeout(unsigned timeout_us, cudaStream_t stream);
  * Synchronizes `stream`, then reads and clears its error word on the current
  * device (stream-ordered; no other stream is waited on). Returns
  * GPTOSS_ATTN_OK, GPTOSS_ATTN_ERR_DEVICE_TIMEOUT, GPTOSS_ATTN_ERR_BAD_POSITION,
- * GPTOSS_ATTN_ERR_BAD_LENGTH or GPTOSS_ATTN_ERR_LAUNCH (a CUDA error surfaced
+ * GPTOSS_ATTN_ERR_BAD_LENGTH, GPTOSS_ATTN_ERR_BAD_PAGE or GPTOSS_ATTN_ERR_LAUNCH (a CUDA error surfaced
  * by the synchronization). While a stream's word holds a timeout, kernels
  * launched on that stream skip their work.
  */
