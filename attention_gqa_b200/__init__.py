@@ -549,9 +549,19 @@ def _paged_int(t, shape, name: str, device):
 
 
 def _paged_device(t: torch.Tensor, what: str) -> torch.device:
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s takes device tensors" % what)
     return t.device
+
+
+def _call_on(device: torch.device, stream, fn, *args) -> int:
+    """fn(*args, stream) with `device` current, on `stream` or the device's current one."""
+    handle = stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, handle)
+    with torch.cuda.device(device):
+        return fn(*args, handle)
 
 
 def paged_append(k, v, pos, kpages, vpages, table, lengths, counts=None, kscales=None,
@@ -580,10 +590,9 @@ def paged_append(k, v, pos, kpages, vpages, table, lengths, counts=None, kscales
     counts_ptr = None if counts is None else _paged_int(counts, (B,), "counts", device)
     lib = _load()
     fn = lib.gptoss_attn_paged_append_yarn if _rope(rope) else lib.gptoss_attn_paged_append
-    with torch.cuda.device(device):
-        st = fn(cache, k.data_ptr(), v.data_ptr(), _step(k, 0), _step(k, 1), _step(v, 0),
-                _step(v, 1), pos_ptr, table_ptr, lengths_ptr, counts_ptr, B, n, max_pages,
-                _stream_handle(stream))
+    st = _call_on(device, stream, fn, cache, k.data_ptr(), v.data_ptr(), _step(k, 0), _step(k, 1),
+                  _step(v, 0), _step(v, 1), pos_ptr, table_ptr, lengths_ptr, counts_ptr, B, n,
+                  max_pages)
     _raise(st, "gptoss_attn_paged_append")
 
 
@@ -621,23 +630,21 @@ def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, p
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
     lib = _load()
     fn = lib.gptoss_attn_paged_attention_yarn if _rope(rope) else lib.gptoss_attn_paged_attention
-    with torch.cuda.device(device):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        made = []
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=device)
-            made.append(out)
-        if workspace is None:
-            workspace = torch.empty(paged_attention_workspace_bytes(B, n), dtype=torch.uint8,
-                                    device=device)
-            made.append(workspace)
-        if stream is not None:
-            for t in made:  # the current stream's, but `stream` uses them
-                t.record_stream(s)
-        st = fn(cache, q4.data_ptr(), _step(q4, 0), _step(q4, 1), pos_ptr, table_ptr,
-                sinks.data_ptr(), lengths_ptr, int(window), out.data_ptr(), B, n, max_pages,
-                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                s.cuda_stream)
+    made = []
+    if out is None:
+        out = q.new_empty(shape)
+        made.append(out)
+    if workspace is None:
+        workspace = torch.empty(lib.gptoss_attn_paged_attention_workspace_bytes(B, n),
+                                dtype=torch.uint8, device=device)
+        made.append(workspace)
+    if stream is not None:
+        for t in made:  # the current stream's, but `stream` uses them
+            t.record_stream(stream)
+    st = _call_on(device, stream, fn, cache, q4.data_ptr(), _step(q4, 0), _step(q4, 1), pos_ptr,
+                  table_ptr, sinks.data_ptr(), lengths_ptr, int(window), out.data_ptr(), B, n,
+                  max_pages, workspace.data_ptr(),
+                  workspace.numel() * workspace.element_size())
     _raise(st, "gptoss_attn_paged_attention")
     return out
 

@@ -206,6 +206,12 @@ int paged_target(int n);
 size_t paged_workspace_bytes(int64_t rows, int n, size_t off[3]);
 cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& args,
                                    cudaStream_t stream);
+// Its kernel for rows of kPagedManyTokens tokens, and the second kernel of both.
+constexpr int kPagedManyTokens = 16;
+cudaError_t launch_paged_attention_many(const PagedMaps& maps, const PagedAttentionArgs& args,
+                                        cudaStream_t stream);
+cudaError_t launch_paged_combine(const PagedAttentionArgs& args, int row_tokens,
+                                 cudaStream_t stream);
 
 // Decode split planning shared by the workspace query and the launch.
 void decode_plan(int batch, int max_len, int window, int* nsplit, int* chunk);

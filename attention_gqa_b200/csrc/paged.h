@@ -16,7 +16,8 @@
 
 namespace gqa {
 
-constexpr int kPagedTile = 64;  // keys per tile of the attention kernel
+constexpr int kPagedTile = 64;   // keys per tile of the attention kernel for few tokens
+constexpr int kPagedTileN = 128;  // and of the one for many
 
 // Keys [lo, hi) that some token of one row of queries sees. A row is up to
 // `nt` tokens of one sequence, the tokens t0 .. of the n newest; token t sits at
@@ -28,29 +29,36 @@ GQA_HD void paged_row_range(int len, int n, int t0, int nt, int window, int* lo,
   *lo = window > 0 && first_idx - window + 1 > 0 ? first_idx - window + 1 : 0;
 }
 
-GQA_HD int paged_row_tiles(int lo, int hi) {
-  return hi > lo ? (hi - 1) / kPagedTile - lo / kPagedTile + 1 : 0;
+GQA_HD int paged_row_tiles(int lo, int hi, int tile) {
+  return hi > lo ? (hi - 1) / tile - lo / tile + 1 : 0;
 }
 
-// Tiles per chunk when all rows together have `total` tiles: about `target`
-// chunks, but no chunk shorter than four tiles while a single wave of
-// CTAs (a quarter of the target) takes the whole work in chunks of four.
+// Rows of at most this many tiles are one chunk: a chunk's own latency is that
+// of many tiles, and a row that is not cut needs no second kernel.
+constexpr int kPagedWhole = 8;
+// No chunk of a longer row has fewer tiles than this, unless the division of its
+// tiles into equal parts leaves one less.
+constexpr int kPagedLeast = 4;
+
+// Tiles per chunk when all rows together have `total` tiles and about `target`
+// chunks are wanted.
 GQA_HD int paged_chunk_tiles(int64_t total, int target) {
-  const int64_t many = (total + target - 1) / target;
-  int64_t one = (total * 4 + target - 1) / target;
-  if (one > 4) one = 4;
-  const int64_t c = many > one ? many : one;
-  return c < 1 ? 1 : static_cast<int>(c);
+  const int64_t c = (total + target - 1) / target;
+  return c < kPagedLeast ? kPagedLeast : static_cast<int>(c);
 }
 
 // Chunks of one row (a row without keys has one too: it writes the zeros).
 GQA_HD int paged_row_chunks(int tiles, int chunk) {
-  return tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
+  return tiles > chunk && tiles > kPagedWhole ? (tiles + chunk - 1) / chunk : 1;
 }
 
-// Chunks of a whole call are at most this many: sum of max(1, ceil(tiles/c))
-// with c >= total/target.
-GQA_HD int64_t paged_max_chunks(int64_t rows, int target) { return rows + target; }
+// Chunks of a whole call are at most this many, when no row has more than `most`
+// tiles: sum of max(1, ceil(tiles/c)), with c >= total/target and c >= kPagedLeast.
+GQA_HD int64_t paged_max_chunks(int64_t rows, int most, int target) {
+  if (most <= kPagedWhole) return rows;
+  const int64_t cut = rows * most / kPagedLeast;
+  return rows + (cut < target ? cut : target);
+}
 
 // Chunks of rows that have more than one: those leave partial sums in the
 // workspace. Such a row has more than c tiles, so ceil(tiles/c) < 2 tiles/c.

@@ -27,32 +27,18 @@
 #include <cfloat>
 #include <cmath>
 
-#include "internal.h"
-#include "paged.h"
-#include "sm100_ptx.cuh"
+#include "paged_common.cuh"
 
 namespace gqa {
 namespace {
 
 constexpr int kWarps = 4;  // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kScaleLog2 = 0.125f * kLog2e;
-// The running maximum follows the scores only when one exceeds it by this much
-// (log2 units): p then stays below 2^8, and most tiles leave the sums alone.
-constexpr float kRescaleThreshold = 8.0f;
-// A running maximum below every score: 2^(kNoMax - x) is 0 for any finite x.
-constexpr float kNoMax = -FLT_MAX;
-
 template <bool kFp8>
 struct Shape {
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kStages = kFp8 ? 6 : 4;
   static constexpr uint32_t kTileBytes = kPagedTile * kHeadDim * kElem;  // one of K or V
-};
-
-struct ScanSlot {
-  int row, split, chunks, part;
 };
 
 template <bool kFp8, int NT>
@@ -98,111 +84,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Four e4m3 codes to two f16x2 words (exact).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(codes));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
-  return v;
-}
-
-// Length of sequence b, clamped to the table; one outside it is reported.
-__device__ __forceinline__ int length_of(const PagedAttentionArgs& a, int b) {
-  int len = __ldg(a.len + b);
-  if (len < 0 || len > a.max_len) {
-    atomicOr(a.err, kErrLength);
-    len = len < 0 ? 0 : a.max_len;
-  }
-  return len;
-}
-
-template <int NT>
-__device__ __forceinline__ int row_tiles(const PagedAttentionArgs& a, int row) {
-  const int b = row / a.groups;
-  int lo, hi;
-  paged_row_range(length_of(a, b), a.n, (row - b * a.groups) * NT, NT, a.window, &lo, &hi);
-  return paged_row_tiles(lo, hi);
-}
-
-__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const uint64_t u = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += u;
-  }
-  return v;
-}
-
-// Finds chunk `cid` of the call. Chunks are counted in the low half of the scanned
-// words and those of rows with several in the high half.
-template <int NT>
-__device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid, uint64_t* sums,
-                                           ScanSlot* slot) {
-  const int t = static_cast<int>(threadIdx.x);
-  const int warp = t >> 5, lane = t & 31;
-  const int per = (a.rows + kThreads - 1) / kThreads;
-  const int r0 = min(a.rows, t * per), r1 = min(a.rows, r0 + per);
-  if (t == 0) slot->row = -1;
-  int first = 0;
-  uint64_t mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    first = row_tiles<NT>(a, r);
-    mine += static_cast<uint64_t>(first);
-  }
-  uint64_t inc = warp_scan(mine, lane);
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  uint64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps + 1; ++w) total += sums[w];
-  const int chunk = paged_chunk_tiles(static_cast<int64_t>(total), a.target);
-
-  mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    const uint64_t n = paged_row_chunks(per == 1 ? first : row_tiles<NT>(a, r), chunk);
-    mine += n | (n > 1 ? n << 32 : 0);
-  }
-  inc = warp_scan(mine, lane);
-  if (lane == 31) sums[kWarps + 1 + warp] = inc;
-  __syncthreads();
-  uint64_t at = inc - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (w < warp) at += sums[kWarps + 1 + w];
-  if (static_cast<uint32_t>(cid) - static_cast<uint32_t>(at) < static_cast<uint32_t>(mine)) {
-    for (int r = r0; r < r1; ++r) {
-      const int n = paged_row_chunks(per == 1 ? first : row_tiles<NT>(a, r), chunk);
-      const int i = cid - static_cast<int>(static_cast<uint32_t>(at));
-      if (i < n) {
-        slot->row = r;
-        slot->split = i;
-        slot->chunks = n;
-        slot->part = static_cast<int>(at >> 32);
-        break;
-      }
-      at += static_cast<uint64_t>(n) | (n > 1 ? static_cast<uint64_t>(n) << 32 : 0);
-    }
-  }
-  __syncthreads();
-  return slot->row >= 0;
-}
-
 template <bool kFp8, int NT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     paged_attention_kernel(const __grid_constant__ PagedMaps maps, const PagedAttentionArgs a) {
   using L = Smem<kFp8, NT>;
   constexpr int kStages = Shape<kFp8>::kStages;
@@ -233,8 +116,8 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0)
     *abort_flag = (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) ? 1 : 0;
   ScanSlot* slot = reinterpret_cast<ScanSlot*>(smem + L::kScan + 2 * 5 * 8);
-  if (!find_chunk<NT>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
-                      reinterpret_cast<uint64_t*>(smem + L::kScan), slot))
+  if (!find_chunk<NT, kPagedTile, kThreads>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
+                                            reinterpret_cast<uint64_t*>(smem + L::kScan), slot))
     return;  // past the call's last chunk
   const bool skip = *abort_flag != 0;
   const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
@@ -245,7 +128,7 @@ __global__ void __launch_bounds__(kThreads)
   const int idx0 = len - a.n + t0;  // index of the row's first token
   int lo, hi, tile_a, tile_b;
   paged_row_range(len, a.n, t0, NT, a.window, &lo, &hi);
-  paged_chunk_range(paged_row_tiles(lo, hi), chunks, slot->split, &tile_a, &tile_b);
+  paged_chunk_range(paged_row_tiles(lo, hi, kPagedTile), chunks, slot->split, &tile_a, &tile_b);
   const int key_a = (lo / kPagedTile + tile_a) * kPagedTile;  // first key of the chunk's tiles
   const int n_tiles = tile_b - tile_a;
   const int page_log2 = a.cache.page_log2;
@@ -262,32 +145,11 @@ __global__ void __launch_bounds__(kThreads)
       const int boxes = kPagedTile / box;
       const int last_page = (hi - 1) >> page_log2;
       const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-      // Lane i holds page number pbase + i of the sequence, and its scales; the
-      // next 32 are loaded while these are used. Pages before the first visible
-      // key or past the last are not looked at: their entries may be unset.
-      struct Entry {
-        int page;
-        float ks, vs;
-      };
-      auto fetch = [&](int pi) {
-        Entry e = {a.cache.num_pages, 1.f, 1.f};
-        if (pi <= last_page && pi >= (lo >> page_log2)) {
-          const int page = __ldg(table + pi);
-          if (paged_page_ok(page, a.cache.num_pages)) {
-            e.page = page;
-            if (kFp8) {
-              e.ks = __ldg(a.cache.k_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
-              e.vs = __ldg(a.cache.v_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
-            }
-          } else {
-            // out of the map's range: the copy fills zeros
-            atomicOr(a.err, kErrPage);
-          }
-        }
-        return e;
-      };
+      // Lane i holds page number pbase + i of the sequence, and its scales; the next
+      // 32 are loaded while these are used.
+      auto fetch = [&](int pi) { return fetch_page<kFp8>(a, table, pi, lo, last_page, g); };
       int pbase = key_a >> page_log2;
-      Entry cur = fetch(pbase + lane), nxt = fetch(pbase + 32 + lane);
+      PageEntry cur = fetch(pbase + lane), nxt = fetch(pbase + 32 + lane);
       int issued = 0;
       for (int i = 0; i < n_tiles; ++i) {
         const int s = i % kStages;
@@ -309,10 +171,10 @@ __global__ void __launch_bounds__(kThreads)
         if (kFp8) {
           const int pw = (key0 + (lane & 3) * 16) >> page_log2;  // page of warp's 16 keys
           const float ks = __shfl_sync(0xffffffffu, cur.ks, (pw - pbase) & 31);
-          const float vs = fmaxf(__shfl_sync(0xffffffffu, cur.vs, (pw - pbase) & 31), 0x1p-100f);
+          const float vs = __shfl_sync(0xffffffffu, cur.vs, (pw - pbase) & 31);
           if (lane < 4)
             *reinterpret_cast<float4*>(smem + L::kPage + (s * kWarps + lane) * 16) =
-                make_float4(ks * kScaleLog2, log2f(vs), 1.f / vs, 0.f);
+                page_factors(ks, vs);
           __syncwarp();
         }
         if (lane == 0)
@@ -672,76 +534,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Joins the chunks of the rows that have several, with the sink, normalises and
-// rounds: `warps` warps of a CTA per output row (token and head), each over every
-// warps-th chunk, two elements a lane.
-template <int NT>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttentionArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  __shared__ float2 part[8][32];
-  __shared__ float2 part_ml[8];
-  const int warps = static_cast<int>(blockDim.x >> 5);
-  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int row = static_cast<int>(blockIdx.x), r = static_cast<int>(blockIdx.y);  // r: tk, head
-  const int tk = r / kNumHeads, h = r % kNumHeads;
-  if (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) return;
-  const int2 meta = a.meta[row];
-  const int b = row / a.groups, t = (row - b * a.groups) * NT + tk;
-  if (meta.y == 1 || t >= a.n) return;
-  const int64_t stride = kNumKvHeads * NT * kGroup;
-  const int64_t first = meta.x * stride + (h / kGroup) * (NT * kGroup) + tk * kGroup + h % kGroup;
-  float M = kNoMax, sum = 0.f, o0 = 0.f, o1 = 0.f;
-  constexpr int kBatch = 8;
-  for (int s0 = warp; s0 < meta.y; s0 += kBatch * warps) {
-    float2 ml[kBatch], v[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int s = s0 + j * warps;
-      ml[j] = make_float2(kNoMax, 0.f);
-      v[j] = make_float2(0.f, 0.f);
-      if (s < meta.y) {
-        ml[j] = a.part_ml[first + s * stride];
-        v[j] = *reinterpret_cast<const float2*>(a.part_o + (first + s * stride) * kHeadDim +
-                                                2 * lane);
-      }
-    }
-    float top = M;
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) top = fmaxf(top, ml[j].x);
-    const float f = ex2_approx(M - top);
-    M = top;
-    sum *= f;
-    o0 *= f;
-    o1 *= f;
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const float fj = ex2_approx(ml[j].x - top);
-      sum = fmaf(fj, ml[j].y, sum);
-      o0 = fmaf(fj, v[j].x, o0);
-      o1 = fmaf(fj, v[j].y, o1);
-    }
-  }
-  part[warp][lane] = make_float2(o0, o1);
-  if (lane == 0) part_ml[warp] = make_float2(M, sum);
-  __syncthreads();
-  if (warp > 0) return;
-  const float sink = __ldg(a.sinks + h) * kLog2e;
-  float Mf = sink;
-  for (int w = 0; w < warps; ++w) Mf = fmaxf(Mf, part_ml[w].x);
-  float den = ex2_approx(sink - Mf);
-  o0 = o1 = 0.f;
-  for (int w = 0; w < warps; ++w) {
-    const float f = ex2_approx(part_ml[w].x - Mf);
-    den = fmaf(f, part_ml[w].y, den);
-    o0 = fmaf(f, part[w][lane].x, o0);
-    o1 = fmaf(f, part[w][lane].y, o1);
-  }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  reinterpret_cast<uint32_t*>(a.out + ((static_cast<int64_t>(b) * a.n + t) * kNumHeads + h) *
-                                          kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
-}
-
 template <bool kFp8, int NT>
 cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStream_t stream) {
   using L = Smem<kFp8, NT>;
@@ -756,53 +548,27 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  // no more chunks than the visible keys can give
+  // the most tiles that a row's visible keys can fill
   const int most = paged_row_tiles(0, a.window > 0 && a.window + NT < a.max_len
-                                          ? a.window + NT + kPagedTile : a.max_len);
-  int64_t chunks = paged_max_chunks(a.rows, a.target);
-  if (static_cast<int64_t>(a.rows) * most < chunks) chunks = static_cast<int64_t>(a.rows) * most;
+                                          ? a.window + NT + kPagedTile : a.max_len, kPagedTile);
+  const int64_t chunks = paged_max_chunks(a.rows, most, a.target);
   cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   e = cudaLaunchKernelEx(&cfg, paged_attention_kernel<kFp8, NT>, maps, a);
-  if (e != cudaSuccess || most == 1) return e;
-  // few output rows: several warps each, since their chunks are many
-  const int warps = static_cast<int64_t>(a.rows) * NT * kNumHeads <= 148 * 8 ? 8 : 2;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.rows), NT * kNumHeads);
-  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT>, a);
+  if (e != cudaSuccess || most <= kPagedWhole) return e;
+  return launch_paged_combine(a, NT, stream);
 }
 
 }  // namespace
 
-int paged_row_tokens(int n) { return n == 1 ? 1 : n == 2 ? 2 : 4; }
-
-// About four waves of three CTAs per SM, eight (one per kv head) to a chunk.
-int paged_target(int n) {
-  (void)n;
-  return 148 * 3 * 4 / kNumKvHeads;
-}
-
-size_t paged_workspace_bytes(int64_t rows, int n, size_t off[3]) {
-  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(n))) * kNumKvHeads *
-                       paged_row_tokens(n) * kGroup;
-  off[0] = 0;
-  off[1] = parts * kHeadDim * sizeof(float);
-  off[2] = off[1] + parts * sizeof(float2);
-  return off[2] + ((static_cast<size_t>(rows) * sizeof(int2) + 15) & ~static_cast<size_t>(15));
-}
-
 cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& a,
                                    cudaStream_t stream) {
-  if (a.cache.fp8) {
-    if (a.n == 1) return launch<true, 1>(maps, a, stream);
-    if (a.n == 2) return launch<true, 2>(maps, a, stream);
-    return launch<true, 4>(maps, a, stream);
+  switch (paged_row_tokens(a.n)) {
+    case 1: return a.cache.fp8 ? launch<true, 1>(maps, a, stream) : launch<false, 1>(maps, a, stream);
+    case 2: return a.cache.fp8 ? launch<true, 2>(maps, a, stream) : launch<false, 2>(maps, a, stream);
+    default: return launch_paged_attention_many(maps, a, stream);
   }
-  if (a.n == 1) return launch<false, 1>(maps, a, stream);
-  if (a.n == 2) return launch<false, 2>(maps, a, stream);
-  return launch<false, 4>(maps, a, stream);
 }
 
 }  // namespace gqa

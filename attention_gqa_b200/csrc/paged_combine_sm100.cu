@@ -1,0 +1,130 @@
+// The second kernel of attention over a paged cache: joins the chunks of rows that
+// were cut (a log-sum-exp merge with the sink counted once), and the sizes that both
+// attention kernels plan with.
+#include "paged_common.cuh"
+
+namespace gqa {
+namespace {
+
+// Joins the chunks of the rows that have several, with the sink, normalises and
+// rounds. A CTA of eight warps takes kHeads heads of one token: with one head, every
+// warp takes each eighth chunk and the warps join at the end (few rows, which may
+// have hundreds of chunks); with eight, a warp takes a head (many rows).
+template <int NT, int kHeads>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttentionArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int kSplit = 8 / kHeads;  // warps per head
+  __shared__ float2 part[8][32];
+  __shared__ float2 part_ml[8];
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int row = static_cast<int>(blockIdx.x);
+  const int r = static_cast<int>(blockIdx.y) * kHeads + warp / kSplit;  // token of the row, head
+  const int tk = r / kNumHeads, h = r % kNumHeads;
+  const int2 meta = a.meta[row];
+  const int b = row / a.groups, t = (row - b * a.groups) * NT + tk;
+  if (meta.y == 1 || t >= a.n || (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout)) return;
+  const int64_t stride = kNumKvHeads * NT * kGroup;
+  const int64_t first = meta.x * stride + (h / kGroup) * (NT * kGroup) + tk * kGroup + h % kGroup;
+  float M = kNoMax, sum = 0.f, o0 = 0.f, o1 = 0.f;
+  constexpr int kBatch = 8;
+  for (int s0 = warp % kSplit; s0 < meta.y; s0 += kBatch * kSplit) {
+    float2 ml[kBatch], v[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int s = s0 + j * kSplit;
+      ml[j] = make_float2(kNoMax, 0.f);
+      v[j] = make_float2(0.f, 0.f);
+      if (s < meta.y) {
+        ml[j] = a.part_ml[first + s * stride];
+        v[j] = *reinterpret_cast<const float2*>(a.part_o + (first + s * stride) * kHeadDim +
+                                                2 * lane);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) top = fmaxf(top, ml[j].x);
+    const float f = ex2_approx(M - top);
+    M = top;
+    sum *= f;
+    o0 *= f;
+    o1 *= f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float fj = ex2_approx(ml[j].x - top);
+      sum = fmaf(fj, ml[j].y, sum);
+      o0 = fmaf(fj, v[j].x, o0);
+      o1 = fmaf(fj, v[j].y, o1);
+    }
+  }
+  const float sink = __ldg(a.sinks + h) * kLog2e;
+  float Mf = fmaxf(sink, M), den;
+  if (kSplit > 1) {
+    part[warp][lane] = make_float2(o0, o1);
+    if (lane == 0) part_ml[warp] = make_float2(M, sum);
+    __syncthreads();
+    if (warp > 0) return;
+    Mf = sink;
+    for (int w = 0; w < kSplit; ++w) Mf = fmaxf(Mf, part_ml[w].x);
+    den = ex2_approx(sink - Mf);
+    o0 = o1 = 0.f;
+    for (int w = 0; w < kSplit; ++w) {
+      const float f = ex2_approx(part_ml[w].x - Mf);
+      den = fmaf(f, part_ml[w].y, den);
+      o0 = fmaf(f, part[w][lane].x, o0);
+      o1 = fmaf(f, part[w][lane].y, o1);
+    }
+  } else {
+    const float f = ex2_approx(M - Mf);
+    den = fmaf(f, sum, ex2_approx(sink - Mf));
+    o0 *= f;
+    o1 *= f;
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  reinterpret_cast<uint32_t*>(a.out + ((static_cast<int64_t>(b) * a.n + t) * kNumHeads + h) *
+                                          kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
+}
+
+template <int NT>
+cudaError_t launch(cudaLaunchConfig_t& cfg, const PagedAttentionArgs& a) {
+  // the first form while its CTAs, one per output row, are few
+  const bool few = static_cast<int64_t>(a.rows) * NT <= 16;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows), NT * (few ? kNumHeads : kNumKvHeads));
+  return few ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT, 1>, a)
+             : cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT, 8>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_combine(const PagedAttentionArgs& a, int row_tokens, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.blockDim = dim3(256);
+  switch (row_tokens) {
+    case 1: return launch<1>(cfg, a);
+    case 2: return launch<2>(cfg, a);
+    default: return launch<kPagedManyTokens>(cfg, a);
+  }
+}
+
+int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
+
+// Few tokens: about four waves of three CTAs per SM; many: one wave of two CTAs.
+// Eight CTAs, one per kv head, make a chunk.
+int paged_target(int n) { return (paged_row_tokens(n) <= 2 ? 148 * 3 * 4 : 148 * 2) / kNumKvHeads; }
+
+size_t paged_workspace_bytes(int64_t rows, int n, size_t off[3]) {
+  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(n))) * kNumKvHeads *
+                       paged_row_tokens(n) * kGroup;
+  off[0] = 0;
+  off[1] = parts * kHeadDim * sizeof(float);
+  off[2] = off[1] + parts * sizeof(float2);
+  return off[2] + ((static_cast<size_t>(rows) * sizeof(int2) + 15) & ~static_cast<size_t>(15));
+}
+
+}  // namespace gqa

@@ -1,0 +1,175 @@
+// Device code that the attention kernels over a paged cache share: constants of the
+// softmax, the search for a CTA's work, and the look-up of pages.
+#pragma once
+
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "paged.h"
+#include "sm100_ptx.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kScaleLog2 = 0.125f * kLog2e;
+// The running maximum follows the scores only when one exceeds it by this much
+// (log2 units): p then stays below 2^8, and most tiles leave the sums alone.
+constexpr float kRescaleThreshold = 8.0f;
+// A running maximum below every score: 2^(kNoMax - x) is 0 for any finite x.
+constexpr float kNoMax = -FLT_MAX;
+
+struct ScanSlot {
+  int row, split, chunks, part;
+};
+
+// Length of sequence b, clamped to the table; one outside it is reported.
+__device__ __forceinline__ int length_of(const PagedAttentionArgs& a, int b) {
+  int len = __ldg(a.len + b);
+  if (len < 0 || len > a.max_len) {
+    atomicOr(a.err, kErrLength);
+    len = len < 0 ? 0 : a.max_len;
+  }
+  return len;
+}
+
+template <int NT, int kTile>
+__device__ __forceinline__ int row_tiles(const PagedAttentionArgs& a, int row) {
+  const int b = row / a.groups;
+  int lo, hi;
+  paged_row_range(length_of(a, b), a.n, (row - b * a.groups) * NT, NT, a.window, &lo, &hi);
+  return paged_row_tiles(lo, hi, kTile);
+}
+
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// Finds chunk `cid` of the call, by all kThreads threads of the CTA; false past the
+// last one. `sums`: two words per warp. Chunks are counted in the low half of the
+// scanned words, those of rows with several in the high half.
+template <int NT, int kTile, int kThreads>
+__device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid, uint64_t* sums,
+                                           ScanSlot* slot) {
+  constexpr int kWarps = kThreads / 32;
+  const int t = static_cast<int>(threadIdx.x);
+  const int warp = t >> 5, lane = t & 31;
+  const int per = (a.rows + kThreads - 1) / kThreads;
+  const int r0 = min(a.rows, t * per), r1 = min(a.rows, r0 + per);
+  if (t == 0) slot->row = -1;
+  int first = 0;
+  uint64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    first = row_tiles<NT, kTile>(a, r);
+    mine += static_cast<uint64_t>(first);
+  }
+  uint64_t inc = warp_scan(mine, lane);
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  uint64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += sums[w];
+  const int chunk = paged_chunk_tiles(static_cast<int64_t>(total), a.target);
+
+  mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const uint64_t n = paged_row_chunks(per == 1 ? first : row_tiles<NT, kTile>(a, r), chunk);
+    mine += n | (n > 1 ? n << 32 : 0);
+  }
+  inc = warp_scan(mine, lane);
+  if (lane == 31) sums[kWarps + warp] = inc;
+  __syncthreads();
+  uint64_t at = inc - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps - 1; ++w)
+    if (w < warp) at += sums[kWarps + w];
+  if (static_cast<uint32_t>(cid) - static_cast<uint32_t>(at) < static_cast<uint32_t>(mine)) {
+    for (int r = r0; r < r1; ++r) {
+      const int n = paged_row_chunks(per == 1 ? first : row_tiles<NT, kTile>(a, r), chunk);
+      const int i = cid - static_cast<int>(static_cast<uint32_t>(at));
+      if (i < n) {
+        slot->row = r;
+        slot->split = i;
+        slot->chunks = n;
+        slot->part = static_cast<int>(at >> 32);
+        break;
+      }
+      at += static_cast<uint64_t>(n) | (n > 1 ? static_cast<uint64_t>(n) << 32 : 0);
+    }
+  }
+  __syncthreads();
+  return slot->row >= 0;
+}
+
+struct PageEntry {
+  int page;
+  float ks, vs;
+};
+
+// Page `pi` of a sequence and its scales for kv head g. Pages before the one of the
+// first visible key `lo`, or past the last, are not looked at (their entries may be
+// unset); a bad number is reported, and stands for a page past the pool, of which
+// copies read zeros.
+template <bool kFp8>
+__device__ __forceinline__ PageEntry fetch_page(const PagedAttentionArgs& a, const int32_t* table,
+                                                int pi, int lo, int last_page, int g) {
+  PageEntry e = {a.cache.num_pages, 1.f, 1.f};
+  if (pi <= last_page && pi >= (lo >> a.cache.page_log2)) {
+    const int page = __ldg(table + pi);
+    if (paged_page_ok(page, a.cache.num_pages)) {
+      e.page = page;
+      if (kFp8) {
+        e.ks = __ldg(a.cache.k_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
+        e.vs = __ldg(a.cache.v_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
+      }
+    } else {
+      atomicOr(a.err, kErrPage);
+    }
+  }
+  return e;
+}
+
+// What the softmax needs of a page's scales: the factor of its scores, log2 of its
+// value scale, and that scale's reciprocal.
+__device__ __forceinline__ float4 page_factors(float ks, float vs) {
+  vs = fmaxf(vs, 0x1p-100f);
+  return make_float4(ks * kScaleLog2, log2f(vs), 1.f / vs, 0.f);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four e4m3 codes to two f16x2 words (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+}  // namespace
+}  // namespace gqa

@@ -407,7 +407,8 @@ size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n);
  * A page number outside [0, num_pages) is reported by check (BAD_PAGE) and read as
  * a page of zeros. What lies in slots that no token sees (later tokens' rows,
  * stale rows, NaN) does not reach the output. Scores, softmax and sums are fp32;
- * rotated q and the probabilities keep 16 (bf16 pages) or 11 bits (e4m3 pages).
+ * rotated q and the probabilities keep 16 bits (bf16 pages; with n > 2 the
+ * probabilities 8) or 11 bits (e4m3 pages).
  * batch >= 1, n >= 1, batch * n <= 131072. One or two kernels on `stream`. How the work
  * is cut depends on the lengths of the whole batch, and the order of the fp32 sums
  * with it.

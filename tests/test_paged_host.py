@@ -15,7 +15,6 @@ import attention_gqa_b200 as gqa
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "attention_gqa_b200", "csrc")
-TILE = 64
 
 SHIM = """
 #include "paged.h"
@@ -24,10 +23,10 @@ extern "C" {
 void row_range(int len, int n, int t0, int nt, int w, int* out) {
   paged_row_range(len, n, t0, nt, w, out, out + 1);
 }
-int row_tiles(int lo, int hi) { return paged_row_tiles(lo, hi); }
+int row_tiles(int lo, int hi, int tile) { return paged_row_tiles(lo, hi, tile); }
 int chunk_tiles(long long total, int target) { return paged_chunk_tiles(total, target); }
 int row_chunks(int tiles, int chunk) { return paged_row_chunks(tiles, chunk); }
-long long max_chunks(long long rows, int target) { return paged_max_chunks(rows, target); }
+long long max_chunks(long long rows, int most, int target) { return paged_max_chunks(rows, most, target); }
 long long max_parts(int target) { return paged_max_parts(target); }
 void chunk_range(int tiles, int chunks, int i, int* out) {
   paged_chunk_range(tiles, chunks, i, out, out + 1);
@@ -48,7 +47,7 @@ def host(tmp_path_factory):
                     str(so)], check=True)
     lib = ctypes.CDLL(str(so))
     lib.max_chunks.restype = lib.max_parts.restype = ctypes.c_longlong
-    lib.max_chunks.argtypes = [ctypes.c_longlong, ctypes.c_int]
+    lib.max_chunks.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
     lib.chunk_tiles.argtypes = [ctypes.c_longlong, ctypes.c_int]
     lib.scale_bits.restype = ctypes.c_uint
     lib.scale_bits.argtypes = [ctypes.c_uint]
@@ -64,8 +63,8 @@ def _pair(fn, *args):
 def test_row_range_is_the_union_of_its_tokens_keys(host):
     rng = random.Random(1)
     for _ in range(3000):
-        n, nt = rng.randint(1, 9), rng.choice((1, 2, 4))
-        length, w = rng.randint(0, 40), rng.choice((0, 0, 1, 2, 5, 39))
+        n, nt = rng.randint(1, 40), rng.choice((1, 2, 4, 16))
+        length, w = rng.randint(0, 60), rng.choice((0, 0, 1, 2, 5, 39))
         t0 = rng.randrange(0, n, nt)
         seen = set()
         for t in range(t0, min(t0 + nt, n)):
@@ -85,14 +84,15 @@ def test_row_range_is_the_union_of_its_tokens_keys(host):
 def test_tiles_cover_a_range(host):
     for lo in (0, 1, 63, 64, 65, 200):
         for hi in range(lo - 2, lo + 200, 7):
-            tiles = {j // TILE for j in range(lo, hi)}
-            assert host.row_tiles(lo, hi) == len(tiles)
+            for tile in (64, 128):
+                tiles = {j // tile for j in range(lo, hi)}
+                assert host.row_tiles(lo, hi, tile) == len(tiles)
 
 
 @pytest.mark.parametrize("target", [37, 222])
 def test_chunks_cover_every_tile_once_within_the_grid_and_the_workspace(host, target):
     rng = random.Random(target)
-    batches = [[0], [1], [0, 0, 0], [2048], [2048] * 64, [1] * 4000, [128] * 64, [129] * 64,
+    batches = [[0], [1], [8], [8, 9], [9] * 64, [0, 0, 0], [2048], [2048] * 64, [1] * 4000, [128] * 64, [129] * 64,
                [4, 5] * 30]
     for _ in range(400):
         rows = rng.choice((1, 2, 7, 64, 300))
@@ -108,10 +108,11 @@ def test_chunks_cover_every_tile_once_within_the_grid_and_the_workspace(host, ta
             at = 0
             for i in range(n):
                 a, b = _pair(host.chunk_range, t, n, i)
-                assert a == at and b >= a and b - a <= c
+                assert a == at and b >= a and (b - a <= c or n == 1)
                 at = b
             assert at == t
-        assert chunks <= host.max_chunks(len(tiles), target)
+        for most in (max(tiles), max(tiles) + 1, 2048):
+            assert chunks <= host.max_chunks(len(tiles), most, target)
         assert parts <= host.max_parts(target)
 
 
