@@ -47,12 +47,25 @@ struct Halves {
       hi[2 * e + 1] = bf16hi_to_f32(hw[e]);
     }
   }
+  // lo cos - hi sin, hi cos + lo sin; as the rotation of the other entry points rounds them
   __device__ __forceinline__ void turn(const Turn& t) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float a = lo[e], h = hi[e];
       lo[e] = fmaf(a, t.c[e], -h * t.s[e]);
       hi[e] = fmaf(h, t.c[e], a * t.s[e]);
+    }
+  }
+  // The same with each result's error an ulp at most (the product's rounding error is
+  // added back): codes are fp32 values rounded once more, so an error of the sum
+  // shows wherever a value lies at a border between two codes.
+  __device__ __forceinline__ void turn_exactly(const Turn& t) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = lo[e], h = hi[e];
+      const float hs = h * t.s[e], as = a * t.s[e];
+      lo[e] = fmaf(a, t.c[e], -hs) + fmaf(-h, t.s[e], hs);
+      hi[e] = fmaf(h, t.c[e], as) + fmaf(a, t.s[e], -as);
     }
   }
 };
@@ -154,82 +167,128 @@ __device__ __forceinline__ uint32_t move_e4m3x4(uint32_t codes, float f) {
   return pack_e4m3x2(a.x * f, a.y * f) | pack_e4m3x2(b.x * f, b.y * f) << 16;
 }
 
-// A CTA per page that a sequence's new tokens touch, a warp per head of its keys
-// (warps 0-7) and of its values (8-15), so a page's scale is one warp's business.
-// A warp goes over its new rows twice, eight at a time (four lanes each): once
-// for the largest value, once to write the codes.
-__global__ void __launch_bounds__(512) append_e4m3_kernel(const PagedAppendArgs a) {
+// The largest |value|, NaN aside; infinite if there is an infinity.
+__device__ __forceinline__ float largest(const Halves& x, float top) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmax3(top, fabsf(x.lo[e]), fabsf(x.hi[e]));
+  return top;
+}
+
+__device__ __forceinline__ float largest_finite(const Halves& x, float top) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float u = fabsf(x.lo[e]), v = fabsf(x.hi[e]);
+    top = fmax3(top, u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f);
+  }
+  return top;
+}
+
+constexpr int kAppendWarps = 16;  // most warps of a CTA
+
+// Two CTAs per page that a sequence's new tokens touch, one for its keys and one for its
+// values. A warp takes every W-th new token of the page, all heads of it, four lanes
+// a head as above (1 KB per load, and one table row for all heads); kTokens is how
+// many that can be. Tokens are read once and kept (the first four; a warp has more only
+// in pages of 128), for the largest value of each head, over the CTA, and then for
+// the codes.
+template <int kTokens>
+__global__ void __launch_bounds__(32 * kAppendWarps, 2)
+    append_e4m3_kernel(const PagedAppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
+  constexpr int kKeep = kTokens < 4 ? kTokens : 4;
+  __shared__ float tops[kAppendWarps][kNumKvHeads];
   const int b = static_cast<int>(blockIdx.y);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int head = warp & 7;
-  const bool is_v = warp >= 8;
-  const int sub = lane >> 2, c = lane & 3;
+  const int warps = static_cast<int>(blockDim.x >> 5);
+  const int head = lane >> 2, c = lane & 3;
+  const bool is_v = (blockIdx.x & 1) != 0;
   int start, count;
   if (!new_tokens(a, b, &start, &count)) return;
   const PagedCache& pc = a.cache;
   const int P = 1 << pc.page_log2;
-  const int pi = (start >> pc.page_log2) + static_cast<int>(blockIdx.x);  // page of the sequence
-  const int base = pi << pc.page_log2;                                    // its first index
+  const int pi = (start >> pc.page_log2) + static_cast<int>(blockIdx.x >> 1);  // of the sequence
+  const int base = pi << pc.page_log2;  // the page's first index
   if (base >= start + count) return;
+  const int s0 = start > base ? start - base : 0;  // slots [s0, s1) are new
+  const int s1 = start + count - base < P ? start + count - base : P;
+  const int t0 = base - start;  // token of slot 0
   const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + pi);
+  const uint16_t* src = (is_v ? a.v + b * a.v_batch : a.k + b * a.k_batch) + head * kHeadDim;
+  const int64_t src_token = is_v ? a.v_token : a.k_token;
+
+  uint4 keep[kKeep][2];  // this lane's chunks c and c+4
+  auto load = [&](int s, uint4 (&w)[2]) {
+    const uint4* p4 = reinterpret_cast<const uint4*>(src + (t0 + s) * src_token);
+    w[0] = __ldg(p4 + c);
+    w[1] = __ldg(p4 + c + 4);
+  };
+  auto value = [&](int s, const uint4 (&w)[2], bool exactly) {
+    Halves x;
+    x.unpack(w[0], w[1]);
+    if (!is_v) {
+      Turn turn;
+      turn.load(table_row(a, b, t0 + s), c);
+      if (exactly) {
+        x.turn_exactly(turn);
+      } else {
+        x.turn(turn);
+      }
+    }
+    return x;
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (s0 + warp + i * warps < s1) load(s0 + warp + i * warps, keep[i]);
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    const int s = s0 + warp + i * warps;
+    if (s >= s1) break;
+    uint4 more[2];
+    if (i >= kKeep) load(s, more);
+    // an ulp on the largest value makes no difference to the codes
+    const Halves x = value(s, i < kKeep ? keep[i < kKeep ? i : 0] : more, false);
+    const float all = largest(x, top);
+    top = all < INFINITY ? all : largest_finite(x, top);
+  }
   if (!paged_page_ok(page, pc.num_pages)) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrPage);
     return;
   }
-  const int s0 = start > base ? start - base : 0;            // slots [s0, s1) are new
-  const int s1 = start + count - base < P ? start + count - base : P;
-  const uint16_t* src = is_v ? a.v + b * a.v_batch : a.k + b * a.k_batch;
-  const int64_t src_token = is_v ? a.v_token : a.k_token;
-  const int64_t at = page * pc.page_stride + head * pc.head_stride;
-  uint8_t* dst = (is_v ? pc.v : pc.k) + at;
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // the scale that the page has, if it holds earlier tokens
   float* scale = (is_v ? pc.v_scale : pc.k_scale) + static_cast<int64_t>(page) * kNumKvHeads + head;
-
-  // this lane's sixteen values of slot s
-  auto row = [&](int s, Halves* x) {
-    const int t = base + s - start;
-    const uint4* p4 = reinterpret_cast<const uint4*>(src + t * src_token + head * kHeadDim);
-    x->unpack(__ldg(p4 + c), __ldg(p4 + c + 4));
-    if (!is_v) {
-      Turn turn;
-      turn.load(table_row(a, b, t), c);
-      x->turn(turn);
-    }
-  };
-  float largest = 0.f;
-  for (int s = s0 + sub; s < s1; s += 8) {
-    Halves x;
-    row(s, &x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float u = fabsf(x.lo[e]), v = fabsf(x.hi[e]);
-      if (u < INFINITY) largest = fmaxf(largest, u);
-      if (v < INFINITY) largest = fmaxf(largest, v);
+  const float before = s0 > 0 ? *scale : 0.f;
+  if (warps > 1) {
+    if (c == 0) tops[warp][head] = top;
+    __syncthreads();  // and every warp has read the scale
+    for (int w = 0; w < warps; ++w) top = fmaxf(top, tops[w][head]);
+  }
+  __syncwarp();
+  const float least = __uint_as_float(paged_scale_bits(__float_as_uint(top)));
+  const float size = before >= least ? before : least;
+  if (warp == 0 && c == 0) *scale = size;
+  uint8_t* dst = (is_v ? pc.v : pc.k) + page * pc.page_stride + head * pc.head_stride;
+  if (size != before) {
+    // it grew (for this lane's head): move the earlier tokens' codes
+    const float f = before / size;
+    for (int s = warp; s < s0; s += warps) {
+      uint4* row4 = reinterpret_cast<uint4*>(dst + s * pc.token_stride) + c;
+      const uint4 w = *row4;
+      *row4 = make_uint4(move_e4m3x4(w.x, f), move_e4m3x4(w.y, f), move_e4m3x4(w.z, f),
+                         move_e4m3x4(w.w, f));
     }
   }
-  largest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(largest)));
-  float size = __uint_as_float(paged_scale_bits(__float_as_uint(largest)));
-  if (s0 > 0) {  // earlier tokens share the page
-    const float before = *scale;
-    if (before >= size) {
-      size = before;
-    } else {
-      const float f = before / size;
-      for (int s = sub; s < s0; s += 8) {
-        uint4* row4 = reinterpret_cast<uint4*>(dst + s * pc.token_stride) + c;
-        const uint4 w = *row4;
-        *row4 = make_uint4(move_e4m3x4(w.x, f), move_e4m3x4(w.y, f), move_e4m3x4(w.z, f),
-                           move_e4m3x4(w.w, f));
-      }
-    }
-  }
-  __syncwarp();  // every lane has read the scale that was there
-  if (lane == 0) *scale = size;
   const float inv = 1.f / size;
-  for (int s = s0 + sub; s < s1; s += 8) {
-    Halves x;
-    row(s, &x);
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    const int s = s0 + warp + i * warps;
+    if (s >= s1) break;
+    uint4 more[2];
+    if (i >= kKeep) load(s, more);
+    const Halves x = value(s, i < kKeep ? keep[i < kKeep ? i : 0] : more, true);
     uint2* row2 = reinterpret_cast<uint2*>(dst + s * pc.token_stride);
     row2[c] = pack_e4m3x8(x.lo, inv);
     row2[c + 4] = pack_e4m3x8(x.hi, inv);
@@ -249,9 +308,16 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   if (a.cache.fp8) {
     // pages that n tokens can touch, wherever in a page they start
     const int P = 1 << a.cache.page_log2;
-    cfg.gridDim = dim3(static_cast<unsigned>((a.n + P - 2) / P + 1), static_cast<unsigned>(a.batch));
-    cfg.blockDim = dim3(512);
-    return cudaLaunchKernelEx(&cfg, append_e4m3_kernel, a);
+    const int most = a.n < P ? a.n : P;  // new tokens in one page
+    int warps = 1;
+    while (warps < kAppendWarps && warps < most) warps *= 2;
+    cfg.gridDim = dim3(2 * static_cast<unsigned>((a.n + P - 2) / P + 1),
+                       static_cast<unsigned>(a.batch));
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
+    if (most <= warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<1>, a);
+    if (most <= 2 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<2>, a);
+    if (most <= 4 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<4>, a);
+    return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<8>, a);
   }
   int warps = 1;
   while (warps < 8 && warps < a.n) warps *= 2;
