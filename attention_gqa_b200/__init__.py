@@ -69,9 +69,6 @@ class _PagedCache(ctypes.Structure):
                 ("type", ctypes.c_int32)]
 
 
-_PAGE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
-
-
 def library_path() -> str:
     return os.path.join(_HERE, _LIB_NAME)
 
@@ -128,7 +125,7 @@ def _load():
     lib.gptoss_attn_paged_append.restype = i32
     lib.gptoss_attn_paged_append_yarn.argtypes = lib.gptoss_attn_paged_append.argtypes
     lib.gptoss_attn_paged_append_yarn.restype = i32
-    lib.gptoss_attn_paged_attention_workspace_bytes.argtypes = [i32, i32]
+    lib.gptoss_attn_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.gptoss_attn_paged_attention_workspace_bytes.restype = sz
     lib.gptoss_attn_paged_attention.argtypes = [cp, vp, i64, i64, vp, vp, vp, vp, i32, vp, i32,
                                                 i32, i32, vp, sz, vp]
@@ -490,77 +487,88 @@ def decode_noalloc(q, kcache, vcache, sinks, lengths, window: int = 0, out=None,
     return out
 
 
-def _heads_at(t: torch.Tensor, heads: int, name: str, device) -> torch.Tensor:
-    """A bf16 [B, n, heads, 64] whose heads and elements are contiguous."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+# The checks of the paged entry points compare what a right call has in one expression
+# and look for the fault only if that fails: a decode step is bound by this host work.
+# Devices are compared by index (-1: host memory).
+_BF16, _I32, _F32, _E4M3 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn
+
+
+def _heads_at(t: torch.Tensor, heads: int, name: str, index: int):
+    """(B, n, batch stride, token stride) of a bf16 [B, n, heads, 64] whose heads and
+    elements are contiguous; strides of dimensions without a second entry are 0."""
+    if t.dtype is _BF16 and t.dim() == 4 and t.get_device() == index:
+        B, n, h, d = t.shape
+        sb, sn, sh, sd = t.stride()
+        if h == heads and d == HEAD_DIM and sh == HEAD_DIM and sd == 1:
+            return B, n, sb if B > 1 else 0, sn if n > 1 else 0
+    if t.dtype != _BF16:
+        raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not on the device of the call" % (name, t.device))
     if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != HEAD_DIM:
         raise ValueError("%s must be [B, n, %d, 64], got %s" % (name, heads, tuple(t.shape)))
-    if t.stride(3) != 1 or t.stride(2) != HEAD_DIM:
-        raise ValueError("%s must have contiguous heads, got strides %s" % (name, t.stride()))
-    return t
+    raise ValueError("%s must have contiguous heads, got strides %s" % (name, t.stride()))
 
 
-def _step(t: torch.Tensor, dim: int) -> int:
-    """Stride of a dimension; 0 where there is nothing to step to."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+def _array(t: torch.Tensor, dtype, shape, name: str, index: int) -> int:
+    """Address of a contiguous array of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not on the device of the call" % (name, t.device))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
 
 
-def _paged_cache(kpages, vpages, kscales, vscales, device) -> _PagedCache:
+def _paged_cache(kpages, vpages, kscales, vscales, index: int) -> _PagedCache:
     """Checks the pages (any strides with contiguous elements) and their scales."""
-    if kpages.dtype not in _PAGE_TYPES:
-        raise TypeError("kpages must be bfloat16 or float8_e4m3fn, got %s" % kpages.dtype)
-    if kpages.dim() != 4 or kpages.shape[1] not in PAGE_SIZES or \
-            kpages.shape[2] != NUM_KV_HEADS or kpages.shape[3] != HEAD_DIM:
+    dtype = kpages.dtype
+    if dtype is not _BF16 and dtype is not _E4M3:
+        raise TypeError("kpages must be bfloat16 or float8_e4m3fn, got %s" % dtype)
+    shape, stride = kpages.shape, kpages.stride()
+    if len(shape) != 4 or shape[1] not in PAGE_SIZES or shape[2] != NUM_KV_HEADS or \
+            shape[3] != HEAD_DIM:
         raise ValueError("kpages must be [num_pages, 16|32|64|128, 8, 64], got %s"
-                         % (tuple(kpages.shape),))
-    if vpages.dtype != kpages.dtype:
-        raise TypeError("vpages must be %s, got %s" % (kpages.dtype, vpages.dtype))
-    stride = kpages.stride()
-    if vpages.shape != kpages.shape or vpages.stride() != stride:
+                         % (tuple(shape),))
+    if vpages.dtype is not dtype:
+        raise TypeError("vpages must be %s, got %s" % (dtype, vpages.dtype))
+    if vpages.shape != shape or vpages.stride() != stride:
         raise ValueError("vpages must have the shape and strides of kpages")
     if stride[3] != 1:
         raise ValueError("the pages' elements must be contiguous, got strides %s" % (stride,))
-    for name, t in (("kpages", kpages), ("vpages", vpages)):
-        if t.device != device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    num_pages, page_size = kpages.shape[0], kpages.shape[1]
-    if kpages.dtype == torch.bfloat16:
+    if kpages.get_device() != index or vpages.get_device() != index:
+        raise ValueError("pages are on %s and %s, not on the device of the call"
+                         % (kpages.device, vpages.device))
+    if dtype is _BF16:
         if kscales is not None or vscales is not None:
             raise ValueError("bf16 pages take no scales")
-        ks = vs = None
-    else:
-        for name, t in (("kscales", kscales), ("vscales", vscales)):
-            if t is None:
-                raise ValueError("float8_e4m3fn pages need %s" % name)
-            if tuple(_dev(t, torch.float32, name, device).shape) != (num_pages, NUM_KV_HEADS):
-                raise ValueError("%s must be [%d, 8], got %s" % (name, num_pages, tuple(t.shape)))
-        ks, vs = kscales.data_ptr(), vscales.data_ptr()
-    return _PagedCache(kpages.data_ptr(), vpages.data_ptr(), ks, vs, stride[0], stride[1],
-                       stride[2], num_pages, page_size, _PAGE_TYPES[kpages.dtype])
+        return _PagedCache(kpages.data_ptr(), vpages.data_ptr(), None, None, stride[0], stride[1],
+                           stride[2], shape[0], shape[1], 0)
+    if kscales is None or vscales is None:
+        raise ValueError("float8_e4m3fn pages need kscales and vscales")
+    scales = (shape[0], NUM_KV_HEADS)
+    return _PagedCache(kpages.data_ptr(), vpages.data_ptr(),
+                       _array(kscales, _F32, scales, "kscales", index),
+                       _array(vscales, _F32, scales, "vscales", index), stride[0], stride[1],
+                       stride[2], shape[0], shape[1], 1)
 
 
-def _paged_int(t, shape, name: str, device):
-    if tuple(_dev(t, torch.int32, name, device).shape) != shape:
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), tuple(t.shape)))
-    return t.data_ptr()
+def _max_pages(table: torch.Tensor) -> int:
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_pages], got %s" % (tuple(table.shape),))
+    return table.shape[1]
 
 
-def _paged_device(t: torch.Tensor, what: str) -> torch.device:
-    if not t.is_cuda:
-        raise ValueError("%s takes device tensors" % what)
-    return t.device
-
-
-def _call_on(device: torch.device, stream, fn, *args) -> int:
-    """fn(*args, stream) with `device` current, on `stream` or the device's current one."""
+def _call_on(index: int, stream, fn, *args) -> int:
+    """fn(*args, stream) with device `index` current, on `stream` or its current one."""
     handle = stream.cuda_stream if stream is not None else \
-        torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+        torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
         return fn(*args, handle)
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return fn(*args, handle)
 
 
@@ -573,31 +581,31 @@ def paged_append(k, v, pos, kpages, vpages, table, lengths, counts=None, kscales
     may be slices of a fused projection. In float8_e4m3fn pages a page's scales
     (a power of two per kv head) follow the largest value that it holds, and are
     written to kscales / vscales [num_pages, 8]. Device tensors only."""
-    device = _paged_device(k, "paged_append")
-    _heads_at(k, NUM_KV_HEADS, "k", device)
-    _heads_at(v, NUM_KV_HEADS, "v", device)
-    if v.shape != k.shape:
+    index = k.get_device()
+    if index < 0:
+        raise ValueError("paged_append takes device tensors")
+    B, n, kb, kt = _heads_at(k, NUM_KV_HEADS, "k", index)
+    vB, vn, vb, vt = _heads_at(v, NUM_KV_HEADS, "v", index)
+    if vB != B or vn != n:
         raise ValueError("v must be %s, got %s" % (tuple(k.shape), tuple(v.shape)))
-    B, n = k.shape[0], k.shape[1]
-    cache = _paged_cache(kpages, vpages, kscales, vscales, device)
-    if table.dim() != 2:
-        raise ValueError("table must be [B, max_pages], got %s" % (tuple(table.shape),))
-    max_pages = table.shape[1]
-    # the tensors themselves stay referenced here until the kernel is enqueued
-    table_ptr = _paged_int(table, (B, max_pages), "table", device)
-    pos_ptr = _paged_int(pos, (B, n), "pos", device)
-    lengths_ptr = _paged_int(lengths, (B,), "lengths", device)
-    counts_ptr = None if counts is None else _paged_int(counts, (B,), "counts", device)
+    cache = _paged_cache(kpages, vpages, kscales, vscales, index)
+    max_pages = _max_pages(table)
+    rows = (B,)
     lib = _load()
     fn = lib.gptoss_attn_paged_append_yarn if _rope(rope) else lib.gptoss_attn_paged_append
-    st = _call_on(device, stream, fn, cache, k.data_ptr(), v.data_ptr(), _step(k, 0), _step(k, 1),
-                  _step(v, 0), _step(v, 1), pos_ptr, table_ptr, lengths_ptr, counts_ptr, B, n,
+    st = _call_on(index, stream, fn, cache, k.data_ptr(), v.data_ptr(), kb, kt, vb, vt,
+                  _array(pos, _I32, (B, n), "pos", index),
+                  _array(table, _I32, (B, max_pages), "table", index),
+                  _array(lengths, _I32, rows, "lengths", index),
+                  None if counts is None else _array(counts, _I32, rows, "counts", index), B, n,
                   max_pages)
-    _raise(st, "gptoss_attn_paged_append")
+    if st != 0:
+        _raise(st, "gptoss_attn_paged_append")
 
 
-def paged_attention_workspace_bytes(batch: int, n: int) -> int:
-    return int(_load().gptoss_attn_paged_attention_workspace_bytes(batch, n))
+def paged_attention_workspace_bytes(batch: int, n: int, max_len: int, window: int = 0) -> int:
+    """Workspace of paged_attention(); 0 where no row of queries can be cut."""
+    return int(_load().gptoss_attn_paged_attention_workspace_bytes(batch, n, max_len, int(window)))
 
 
 def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, pos=None,
@@ -608,44 +616,47 @@ def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, p
     to itself (the last `window` of them if window > 0), and is rotated at `pos`
     [B, n], by default its index; its own key and value are in the pages already.
     Table entries of pages without visible keys may be unset. Device tensors only."""
-    device = _paged_device(q, "paged_attention")
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("paged_attention takes device tensors")
     single = q.dim() == 3
-    q4 = _heads_at(q.unsqueeze(1) if single else q, NUM_HEADS, "q", device)
-    B, n = q4.shape[0], q4.shape[1]
-    cache = _paged_cache(kpages, vpages, kscales, vscales, device)
-    if table.dim() != 2:
-        raise ValueError("table must be [B, max_pages], got %s" % (tuple(table.shape),))
-    max_pages = table.shape[1]
-    # the tensors themselves stay referenced here: their memory must not serve the
-    # allocations below
-    table_ptr = _paged_int(table, (B, max_pages), "table", device)
-    lengths_ptr = _paged_int(lengths, (B,), "lengths", device)
-    pos_ptr = None if pos is None else _paged_int(pos, (B, n), "pos", device)
-    if tuple(_dev(sinks, torch.float32, "sinks", device).shape) != (NUM_HEADS,):
-        raise ValueError("sinks must be [64], got %s" % (tuple(sinks.shape),))
+    B, n, qb, qt = _heads_at(q.unsqueeze(1) if single else q, NUM_HEADS, "q", index)
+    cache = _paged_cache(kpages, vpages, kscales, vscales, index)
+    max_pages = _max_pages(table)
+    # `table`, `lengths`, `pos` and `sinks` stay referenced by their names until the call:
+    # the memory of a temporary must not serve the allocations below
+    table_at = _array(table, _I32, (B, max_pages), "table", index)
+    lengths_at = _array(lengths, _I32, (B,), "lengths", index)
+    sinks_at = _array(sinks, _F32, (NUM_HEADS,), "sinks", index)
+    pos_at = None if pos is None else _array(pos, _I32, (B, n), "pos", index)
     shape = (B, NUM_HEADS, HEAD_DIM) if single else (B, n, NUM_HEADS, HEAD_DIM)
-    if out is not None and tuple(_dev(out, torch.bfloat16, "out", device).shape) != shape:
-        raise ValueError("out must be %s, got %s" % (list(shape), tuple(out.shape)))
-    if workspace is not None and not (workspace.device == device and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    window = int(window)
     lib = _load()
     fn = lib.gptoss_attn_paged_attention_yarn if _rope(rope) else lib.gptoss_attn_paged_attention
     made = []
     if out is None:
         out = q.new_empty(shape)
         made.append(out)
+        out_at = out.data_ptr()
+    else:
+        out_at = _array(out, _BF16, shape, "out", index)
     if workspace is None:
-        workspace = torch.empty(lib.gptoss_attn_paged_attention_workspace_bytes(B, n),
-                                dtype=torch.uint8, device=device)
-        made.append(workspace)
+        need = lib.gptoss_attn_paged_attention_workspace_bytes(
+            B, n, max_pages * cache.page_size, window)
+        if need:
+            workspace = q.new_empty(need // 2)
+            made.append(workspace)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the call")
     if stream is not None:
         for t in made:  # the current stream's, but `stream` uses them
             t.record_stream(stream)
-    st = _call_on(device, stream, fn, cache, q4.data_ptr(), _step(q4, 0), _step(q4, 1), pos_ptr,
-                  table_ptr, sinks.data_ptr(), lengths_ptr, int(window), out.data_ptr(), B, n,
-                  max_pages, workspace.data_ptr(),
-                  workspace.numel() * workspace.element_size())
-    _raise(st, "gptoss_attn_paged_attention")
+    ws_at, ws_bytes = (None, 0) if workspace is None else \
+        (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = _call_on(index, stream, fn, cache, q.data_ptr(), qb, qt, pos_at, table_at, sinks_at,
+                  lengths_at, window, out_at, B, n, max_pages, ws_at, ws_bytes)
+    if st != 0:
+        _raise(st, "gptoss_attn_paged_attention")
     return out
 
 

@@ -612,9 +612,16 @@ static int paged_rows(int batch, int n) {
   return batch * ((n + nt - 1) / nt);
 }
 
-size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n) {
+// A window that covers the longest sequence is full causal.
+static int paged_window(int window, int max_len) {
+  return window > 0 && window < max_len ? window : 0;
+}
+
+size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n, int max_len, int window) {
+  if (!paged_sizes_ok(batch, n) || max_len < 1 || max_len > kMaxPosition) return 0;
   size_t off[3];
-  return paged_sizes_ok(batch, n) ? paged_workspace_bytes(paged_rows(batch, n), n, off) : 0;
+  return paged_workspace_bytes(paged_rows(batch, n), n, max_len, paged_window(window, max_len),
+                               off);
 }
 
 static int paged_attention_impl(const gptoss_attn_paged_cache* cache, const void* q,
@@ -623,7 +630,7 @@ static int paged_attention_impl(const gptoss_attn_paged_cache* cache, const void
                                 int window, void* out, int batch, int n, int max_pages,
                                 void* workspace, size_t workspace_bytes, cudaStream_t stream,
                                 Rope rope) {
-  if (!q || !table || !sinks || !len || !out || !workspace) return GPTOSS_ATTN_ERR_NULL_PTR;
+  if (!q || !table || !sinks || !len || !out) return GPTOSS_ATTN_ERR_NULL_PTR;
   PagedAttentionArgs a;
   int st = paged_view(cache, max_pages, &a.cache);
   if (st != GPTOSS_ATTN_OK) return st;
@@ -632,9 +639,12 @@ static int paged_attention_impl(const gptoss_attn_paged_cache* cache, const void
       misaligned4(pos) || misaligned4(table) || misaligned4(sinks) || misaligned4(len))
     return GPTOSS_ATTN_ERR_BAD_ALIGN;
   a.rows = paged_rows(batch, n);
+  a.max_len = max_pages << a.cache.page_log2;
+  a.window = paged_window(window, a.max_len);
   size_t off[3];
-  if (workspace_bytes < paged_workspace_bytes(a.rows, n, off))
-    return GPTOSS_ATTN_ERR_SMALL_WORKSPACE;
+  const size_t need = paged_workspace_bytes(a.rows, n, a.max_len, a.window, off);
+  if (need && !workspace) return GPTOSS_ATTN_ERR_NULL_PTR;
+  if (workspace_bytes < need) return GPTOSS_ATTN_ERR_SMALL_WORKSPACE;
   int dev = 0;
   st = current_device(&dev);
   if (st == GPTOSS_ATTN_OK) st = ensure_state(dev, rope);
@@ -663,16 +673,13 @@ static int paged_attention_impl(const gptoss_attn_paged_cache* cache, const void
   a.rope = table_of(dev, rope);
   a.out = static_cast<uint16_t*>(out);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.part_o = reinterpret_cast<float*>(ws + off[0]);
-  a.part_ml = reinterpret_cast<float2*>(ws + off[1]);
-  a.meta = reinterpret_cast<int2*>(ws + off[2]);
+  a.part_o = need ? reinterpret_cast<float*>(ws + off[0]) : nullptr;
+  a.part_ml = need ? reinterpret_cast<float2*>(ws + off[1]) : nullptr;
+  a.meta = need ? reinterpret_cast<int2*>(ws + off[2]) : nullptr;
   a.err = err_word(dev, stream);
   a.batch = batch;
   a.n = n;
   a.max_pages = max_pages;
-  a.max_len = max_pages << c.page_log2;
-  // A window covering the longest sequence is full causal.
-  a.window = window > 0 && window < a.max_len ? window : 0;
   a.groups = a.rows / batch;
   a.target = paged_target(n);
   return launch_paged_attention(maps, a, stream) == cudaSuccess ? GPTOSS_ATTN_OK

@@ -188,7 +188,7 @@ struct PagedAttentionArgs {
   uint16_t* out;           // [B][n][64][64] bf16
   float* part_o;           // [part][8][NT * 8][64]: unnormalised sums of a chunk
   float2* part_ml;         // [part][8][NT * 8] (max in log2 units, sum)
-  int2* meta;              // [rows] (first part, chunks)
+  int2* meta;              // [rows] (first part, chunks); the three: nullptr if no row is cut
   int* err;
   int batch, n, max_pages, max_len, window;
   int groups;              // rows (token groups) per sequence
@@ -203,7 +203,10 @@ struct PagedMaps {
 // Query tokens a row holds, chunks aimed for, and the workspace they need.
 int paged_row_tokens(int n);
 int paged_target(int n);
-size_t paged_workspace_bytes(int64_t rows, int n, size_t off[3]);
+// Most tiles that a row can have, whatever the lengths; rows of few tiles are not cut,
+// and then there is no workspace and no second kernel.
+int paged_most_tiles(int n, int max_len, int window);
+size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]);
 cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& args,
                                    cudaStream_t stream);
 // Its kernel for rows of kPagedManyTokens tokens, and the second kernel of both.

@@ -37,7 +37,7 @@ constexpr int kThreads = (kWarps + 1) * 32;
 template <bool kFp8>
 struct Shape {
   static constexpr int kElem = kFp8 ? 1 : 2;
-  static constexpr int kStages = kFp8 ? 6 : 4;
+  static constexpr int kStages = 4;
   static constexpr uint32_t kTileBytes = kPagedTile * kHeadDim * kElem;  // one of K or V
 };
 
@@ -85,7 +85,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 }
 
 template <bool kFp8, int NT>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
     paged_attention_kernel(const __grid_constant__ PagedMaps maps, const PagedAttentionArgs a) {
   using L = Smem<kFp8, NT>;
   constexpr int kStages = Shape<kFp8>::kStages;
@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     return;  // past the call's last chunk
   const bool skip = *abort_flag != 0;
   const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
-  if (slot->split == 0 && g == 0 && threadIdx.x == 0) a.meta[row] = make_int2(slot->part, chunks);
+  if (a.meta && slot->split == 0 && g == 0 && threadIdx.x == 0)
+    a.meta[row] = make_int2(slot->part, chunks);
   const int b = row / a.groups;
   const int t0 = (row - b * a.groups) * NT;
   const int len = min(max(__ldg(a.len + b), 0), a.max_len);
@@ -537,9 +538,9 @@ __global__ void __launch_bounds__(kThreads, 3)
 template <bool kFp8, int NT>
 cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStream_t stream) {
   using L = Smem<kFp8, NT>;
-  cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<kFp8, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(L::kBytes));
+  static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its shared memory
+  cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_attention_kernel<kFp8, NT>), L::kBytes,
+                               &prepared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -548,9 +549,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  // the most tiles that a row's visible keys can fill
-  const int most = paged_row_tiles(0, a.window > 0 && a.window + NT < a.max_len
-                                          ? a.window + NT + kPagedTile : a.max_len, kPagedTile);
+  const int most = paged_most_tiles(a.n, a.max_len, a.window);
   const int64_t chunks = paged_max_chunks(a.rows, most, a.target);
   cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
   cfg.blockDim = dim3(kThreads);

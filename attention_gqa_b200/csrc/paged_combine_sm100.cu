@@ -118,12 +118,21 @@ int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
 // Eight CTAs, one per kv head, make a chunk.
 int paged_target(int n) { return (paged_row_tokens(n) <= 2 ? 148 * 3 * 4 : 148 * 2) / kNumKvHeads; }
 
-size_t paged_workspace_bytes(int64_t rows, int n, size_t off[3]) {
+int paged_most_tiles(int n, int max_len, int window) {
+  const int nt = paged_row_tokens(n);
+  const int tile = nt <= 2 ? kPagedTile : kPagedTileN;
+  // a row of nt tokens sees window + nt - 1 keys, from anywhere in a tile
+  return paged_row_tiles(0, window > 0 && window + nt + tile < max_len ? window + nt + tile : max_len,
+                         tile);
+}
+
+size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]) {
   const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(n))) * kNumKvHeads *
                        paged_row_tokens(n) * kGroup;
   off[0] = 0;
   off[1] = parts * kHeadDim * sizeof(float);
   off[2] = off[1] + parts * sizeof(float2);
+  if (paged_most_tiles(n, max_len, window) <= kPagedWhole) return 0;
   return off[2] + ((static_cast<size_t>(rows) * sizeof(int2) + 15) & ~static_cast<size_t>(15));
 }
 

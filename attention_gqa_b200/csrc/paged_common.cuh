@@ -2,6 +2,7 @@
 // softmax, the search for a CTA's work, and the look-up of pages.
 #pragma once
 
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -20,6 +21,19 @@ constexpr float kScaleLog2 = 0.125f * kLog2e;
 constexpr float kRescaleThreshold = 8.0f;
 // A running maximum below every score: 2^(kNoMax - x) is 0 for any finite x.
 constexpr float kNoMax = -FLT_MAX;
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device.
+inline cudaError_t allow_shared(const void* kernel, uint32_t bytes, std::atomic<uint64_t>* prepared) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (prepared->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess) prepared->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct ScanSlot {
   int row, split, chunks, part;

@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;  // past the call's last chunk
   const bool skip = *ctx.abort_flag != 0;
   const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
-  if (slot->split == 0 && g == 0 && threadIdx.x == 0) a.meta[row] = make_int2(slot->part, chunks);
+  if (a.meta && slot->split == 0 && g == 0 && threadIdx.x == 0)
+    a.meta[row] = make_int2(slot->part, chunks);
   const int b = row / a.groups;
   const int t0 = (row - b * a.groups) * kNT;
   const int len = min(max(__ldg(a.len + b), 0), a.max_len);
@@ -689,9 +690,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <bool kFp8>
 cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStream_t stream) {
   using L = Smem<kFp8>;
-  cudaError_t e = cudaFuncSetAttribute(paged_many_kernel<kFp8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(L::kBytes));
+  static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its shared memory
+  cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_many_kernel<kFp8>), L::kBytes,
+                               &prepared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -700,9 +701,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  // the most tiles that a row's visible keys can fill
-  const int most = paged_row_tiles(0, a.window > 0 && a.window + kNT < a.max_len
-                                          ? a.window + kNT + kTile : a.max_len, kTile);
+  const int most = paged_most_tiles(a.n, a.max_len, a.window);
   const int64_t chunks = paged_max_chunks(a.rows, most, a.target);
   cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
   cfg.blockDim = dim3(kThreads);

@@ -382,10 +382,11 @@ int gptoss_attn_paged_append_yarn(const gptoss_attn_paged_cache* cache, const vo
                                   cudaStream_t stream);
 
 /*
- * Bytes of device workspace gptoss_attn_paged_attention() needs; it does not
- * depend on the capacity of the cache. Returns 0 for invalid sizes.
+ * Bytes of device workspace gptoss_attn_paged_attention() needs when no sequence
+ * is longer than max_len (= max_pages * page_size): 0 where none is (short
+ * sequences or windows), else the same for every max_len. 0 for invalid sizes, too.
  */
-size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n);
+size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n, int max_len, int window);
 
 /*
  * Attention of the n newest tokens of each sequence over its pages (n = 1: a decode
@@ -402,8 +403,9 @@ size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n);
  *           and reported by check as BAD_LENGTH)
  *   sinks   fp32 [64]; -inf allowed
  *   out     bf16 [batch][n][64][64], contiguous
- *   workspace of gptoss_attn_paged_attention_workspace_bytes(batch, n) bytes, 16-byte
- *           aligned, uninitialised; calls that overlap in time need separate ones
+ *   workspace of gptoss_attn_paged_attention_workspace_bytes(batch, n, max_pages *
+ *           page_size, window) bytes (NULL where that is 0), 16-byte aligned,
+ *           uninitialised; calls that overlap in time need separate ones
  * A page number outside [0, num_pages) is reported by check (BAD_PAGE) and read as
  * a page of zeros. What lies in slots that no token sees (later tokens' rows,
  * stale rows, NaN) does not reach the output. Scores, softmax and sums are fp32;

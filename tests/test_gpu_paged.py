@@ -632,7 +632,8 @@ def test_attention_canaries_and_repeat(cuda_device, n):
     cache = Cache(lengths, 32, torch.bfloat16)
     cache.fill(lengths, g)
     q, sinks = _queries(3, n, g)
-    need = gqa.paged_attention_workspace_bytes(3, n)
+    need = gqa.paged_attention_workspace_bytes(3, n, cache.table.shape[1] * 32)
+    assert need > 0
     ws = torch.full((need + 8192,), 0xFF, dtype=torch.uint8, device="cuda")
     buf = torch.full((3 * n * 4096 + 2048,), 2.5, dtype=torch.bfloat16, device="cuda")
     out = buf[1024:1024 + 3 * n * 4096].view(3, n, 64, 64)

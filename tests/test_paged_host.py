@@ -192,10 +192,11 @@ def _append(lib, cache=None, fn="gptoss_attn_paged_append", **kw):
 
 def _attention(lib, cache=None, fn="gptoss_attn_paged_attention", **kw):
     a = dict(q=16, qb=4096, qt=4096, pos=None, table=80, sinks=64, len=96, window=0, out=112,
-             batch=2, n=3, max_pages=4, ws=128, bytes=None)
+             batch=2, n=3, max_pages=80, ws=128, bytes=None)
     a.update(kw)
     if a["bytes"] is None:
-        a["bytes"] = lib.gptoss_attn_paged_attention_workspace_bytes(a["batch"], a["n"])
+        a["bytes"] = lib.gptoss_attn_paged_attention_workspace_bytes(
+            a["batch"], a["n"], max(1, min(131072, a["max_pages"] * 16)), a["window"])
     return getattr(lib, fn)(cache if cache is not None else _cache(), a["q"], a["qb"], a["qt"],
                             a["pos"], a["table"], a["sinks"], a["len"], a["window"], a["out"],
                             a["batch"], a["n"], a["max_pages"], a["ws"], a["bytes"], None)
@@ -223,16 +224,23 @@ def test_attention_argument_errors(lib, fn):
     for change in (dict(q=24), dict(out=120), dict(ws=136), dict(qt=4100), dict(pos=66),
                    dict(table=82), dict(sinks=65), dict(len=98)):
         assert _attention(lib, fn=fn, **change) == BAD_ALIGN, change
-    need = lib.gptoss_attn_paged_attention_workspace_bytes(2, 3)
-    assert _attention(lib, fn=fn, bytes=need - 1) == SMALL
+    need = lib.gptoss_attn_paged_attention_workspace_bytes(2, 3, 1280, 0)
+    assert need > 0 and _attention(lib, fn=fn, bytes=need - 1) == SMALL
 
 
 def test_attention_workspace_query(lib):
     ws = lib.gptoss_attn_paged_attention_workspace_bytes
     for batch, n in ((0, 1), (1, 0), (-1, 1), (1, -1), (131073, 1), (1, 131073), (512, 257)):
-        assert ws(batch, n) == 0
-    assert 0 < ws(1, 1) <= ws(64, 1) <= ws(131072, 1)
-    assert ws(64, 1) < 16 << 20  # bounded by the chunks, not by the cache
+        assert ws(batch, n, 8192, 0) == 0
+    for length in (0, -1, 131073):
+        assert ws(1, 1, length, 0) == 0
+    assert 0 < ws(1, 1, 8192, 0) <= ws(64, 1, 8192, 0) <= ws(131072, 1, 8192, 0)
+    assert ws(64, 1, 8192, 0) == ws(64, 1, 131072, 0) < 16 << 20  # the chunks', not the cache's
+    # none where no row of queries is cut: up to 8 tiles (of 64 keys; of 128 beyond two tokens)
+    assert ws(64, 1, 512, 0) == 0 < ws(64, 1, 528, 0)
+    assert ws(64, 1, 131072, 128) == 0 < ws(64, 1, 131072, 1000)
+    assert ws(64, 3, 1024, 0) == 0 < ws(64, 3, 1040, 0)
+    assert ws(64, 3, 131072, 128) == 0
 
 
 # -------------------------------------------------------------- Python refusals
@@ -241,14 +249,17 @@ def _pages(dtype=torch.bfloat16, num=4, page=16):
     return torch.zeros(num, page, 8, 64, dtype=torch.uint8).to(dtype)
 
 
+HOST = -1  # device index of host tensors
+
+
 def test_binding_refuses_bad_pages():
-    cpu = torch.device("cpu")
     e4 = torch.float8_e4m3fn
     p, s = _pages(), torch.ones(4, 8)
     for args, kind in [
         ((_pages(torch.float32), p, None, None), TypeError),
         ((p, _pages(e4), None, None), TypeError),
         ((_pages(page=24), _pages(page=24), None, None), ValueError),
+        ((p[0], p[0], None, None), ValueError),
         ((p[:, :, :4], p[:, :, :4], None, None), ValueError),
         ((p, _pages(num=5), None, None), ValueError),
         ((p, torch.zeros(4, 8, 16, 64, dtype=torch.bfloat16).transpose(1, 2), None, None), ValueError),
@@ -260,26 +271,36 @@ def test_binding_refuses_bad_pages():
         ((_pages(e4), _pages(e4), s, torch.ones(8, 4).t()), ValueError),
     ]:
         with pytest.raises(kind):
-            gqa._paged_cache(*args, cpu)
+            gqa._paged_cache(*args, HOST)
+    with pytest.raises(ValueError, match="device"):
+        gqa._paged_cache(p, p, None, None, 0)
     view = torch.zeros(4, 8, 16, 64, dtype=torch.bfloat16).transpose(1, 2)  # laid out by head
-    c = gqa._paged_cache(view, view, None, None, cpu)
+    c = gqa._paged_cache(view, view, None, None, HOST)
     assert (c.page_stride, c.token_stride, c.head_stride, c.page_size) == (8192, 64, 1024, 16)
+    assert (c.num_pages, c.type, c.k_scale) == (4, 0, None)
+    c = gqa._paged_cache(_pages(e4), _pages(e4), s, s, HOST)
+    assert (c.type, c.k_scale, c.v_scale) == (1, s.data_ptr(), s.data_ptr())
 
 
 def test_binding_refuses_bad_tokens():
-    cpu = torch.device("cpu")
     qkv = torch.zeros(2, 3, 80, 64, dtype=torch.bfloat16)
-    assert gqa._heads_at(qkv[:, :, 64:72], 8, "k", cpu).stride(1) == 80 * 64
+    assert gqa._heads_at(qkv[:, :, 64:72], 8, "k", HOST) == (2, 3, 3 * 80 * 64, 80 * 64)
+    assert gqa._heads_at(qkv[:1, 1:2, :64], 64, "q", HOST) == (1, 1, 0, 0)
     for t, kind in ((qkv.float()[:, :, :8], TypeError), (qkv, ValueError), (qkv[0, :, :8], ValueError),
                     (qkv[:, :, :16:2], ValueError), (qkv[:, :, :8, :32], ValueError),
                     (torch.zeros(2, 3, 64, 8, dtype=torch.bfloat16).transpose(2, 3), ValueError)):
         with pytest.raises(kind):
-            gqa._heads_at(t, 8, "k", cpu)
+            gqa._heads_at(t, 8, "k", HOST)
+    with pytest.raises(ValueError, match="device"):
+        gqa._heads_at(qkv[:, :, :8], 8, "k", 0)
     x = torch.zeros(2, dtype=torch.int32)
-    assert gqa._paged_int(x, (2,), "lengths", cpu) == x.data_ptr()
-    for t, kind in ((x.long(), TypeError), (x[:1], ValueError), (torch.zeros(4, dtype=torch.int32)[::2], ValueError)):
+    assert gqa._array(x, torch.int32, (2,), "lengths", HOST) == x.data_ptr()
+    for t, kind in ((x.long(), TypeError), (x[:1], ValueError), (x[:, None], ValueError),
+                    (torch.zeros(4, dtype=torch.int32)[::2], ValueError)):
         with pytest.raises(kind):
-            gqa._paged_int(t, (2,), "lengths", cpu)
+            gqa._array(t, torch.int32, (2,), "lengths", HOST)
+    with pytest.raises(ValueError, match="device"):
+        gqa._array(x, torch.int32, (2,), "lengths", 0)
 
 
 def test_binding_takes_device_tensors_only(monkeypatch):
