@@ -203,9 +203,9 @@ struct PagedMaps {
 // Query tokens a row holds, chunks aimed for, and the workspace they need.
 int paged_row_tokens(int n);
 int paged_target(int n);
-// Most tiles that a row can have, whatever the lengths; rows of few tiles are not cut,
+// Most tiles that a row can have, whatever the lengths. Rows of few tiles are not cut,
 // and then there is no workspace and no second kernel.
-int paged_most_tiles(int n, int max_len, int window);
+int paged_most_tiles(int row_tokens, int tile, int max_len, int window);
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]);
 cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& args,
                                    cudaStream_t stream);

@@ -34,11 +34,15 @@ namespace {
 
 constexpr int kWarps = 4;  // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
+// Sixteen-key blocks a warp takes of a tile: two for e4m3, whose work per byte is
+// twice as much, so that the waits and indices of a tile serve 32 keys.
 template <bool kFp8>
 struct Shape {
   static constexpr int kElem = kFp8 ? 1 : 2;
-  static constexpr int kStages = 4;
-  static constexpr uint32_t kTileBytes = kPagedTile * kHeadDim * kElem;  // one of K or V
+  static constexpr int kBlocks = kFp8 ? 2 : 1;
+  static constexpr int kTile = 16 * kWarps * kBlocks;  // keys
+  static constexpr int kStages = kFp8 ? 3 : 4;
+  static constexpr uint32_t kTileBytes = kTile * kHeadDim * kElem;  // one of K or V
 };
 
 template <bool kFp8, int NT>
@@ -52,8 +56,10 @@ struct Smem {
   static constexpr uint32_t kEnd0 = kTiles > kWarps * kMergeWarp ? kTiles : kWarps * kMergeWarp;
   static constexpr uint32_t kQ = kEnd0;  // 16-bit [2][NT][8][64] (the second half: bf16 only)
   static constexpr uint32_t kQExp = kQ + (kFp8 ? 1 : 2) * NT * kGroup * kHeadDim * 2;  // [NT][8]
-  static constexpr uint32_t kPage = kQExp + NT * kGroup * 4;  // float4 [stages][4 warps], e4m3
-  static constexpr uint32_t kBar = kPage + (kFp8 ? Shape<kFp8>::kStages * kWarps * 16 : 0);
+  // float4 [stages][blocks of a tile], e4m3
+  static constexpr int kPages = kFp8 ? kWarps * Shape<kFp8>::kBlocks : 0;
+  static constexpr uint32_t kPage = kQExp + NT * kGroup * 4;
+  static constexpr uint32_t kBar = kPage + Shape<kFp8>::kStages * kPages * 16;
   static constexpr uint32_t kScan = kBar + 2 * Shape<kFp8>::kStages * 8;  // 5 + 5 warp sums, slot
   static constexpr uint32_t kMisc = kScan + 2 * 5 * 8 + 16;
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
@@ -85,10 +91,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 }
 
 template <bool kFp8, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : 4)
     paged_attention_kernel(const __grid_constant__ PagedMaps maps, const PagedAttentionArgs a) {
   using L = Smem<kFp8, NT>;
   constexpr int kStages = Shape<kFp8>::kStages;
+  constexpr int kTile = Shape<kFp8>::kTile;
+  constexpr int kBlocks = Shape<kFp8>::kBlocks;
   constexpr uint32_t kTileBytes = Shape<kFp8>::kTileBytes;
   constexpr uint32_t kRowBytes = kHeadDim * Shape<kFp8>::kElem;
   griddep_launch_dependents();
@@ -116,8 +124,8 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
   if (threadIdx.x == 0)
     *abort_flag = (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) ? 1 : 0;
   ScanSlot* slot = reinterpret_cast<ScanSlot*>(smem + L::kScan + 2 * 5 * 8);
-  if (!find_chunk<NT, kPagedTile, kThreads>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
-                                            reinterpret_cast<uint64_t*>(smem + L::kScan), slot))
+  if (!find_chunk<NT, kTile, kThreads>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
+                                       reinterpret_cast<uint64_t*>(smem + L::kScan), slot))
     return;  // past the call's last chunk
   const bool skip = *abort_flag != 0;
   const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
@@ -129,8 +137,8 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
   const int idx0 = len - a.n + t0;  // index of the row's first token
   int lo, hi, tile_a, tile_b;
   paged_row_range(len, a.n, t0, NT, a.window, &lo, &hi);
-  paged_chunk_range(paged_row_tiles(lo, hi, kPagedTile), chunks, slot->split, &tile_a, &tile_b);
-  const int key_a = (lo / kPagedTile + tile_a) * kPagedTile;  // first key of the chunk's tiles
+  paged_chunk_range(paged_row_tiles(lo, hi, kTile), chunks, slot->split, &tile_a, &tile_b);
+  const int key_a = (lo / kTile + tile_a) * kTile;  // first key of the chunk's tiles
   const int n_tiles = tile_b - tile_a;
   const int page_log2 = a.cache.page_log2;
 
@@ -143,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
       }
       const int P = 1 << page_log2;
       const int box = P < kPagedTile ? P : kPagedTile;  // keys per copy
-      const int boxes = kPagedTile / box;
+      const int boxes = kTile / box;                    // at most 8
       const int last_page = (hi - 1) >> page_log2;
       const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
       // Lane i holds page number pbase + i of the sequence, and its scales; the next
@@ -151,30 +159,30 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
       auto fetch = [&](int pi) { return fetch_page<kFp8>(a, table, pi, lo, last_page, g); };
       int pbase = key_a >> page_log2;
       PageEntry cur = fetch(pbase + lane), nxt = fetch(pbase + 32 + lane);
+      const int sub = lane & 7;
       int issued = 0;
+      int s = 0;             // stage of tile i
+      uint32_t phase = 1;    // parity of its release before; a fresh barrier passes at once
       for (int i = 0; i < n_tiles; ++i) {
-        const int s = i % kStages;
-        const int key0 = key_a + i * kPagedTile;
+        const int key0 = key_a + i * kTile;
         if ((key0 >> page_log2) >= pbase + 32) {
           pbase += 32;
           cur = nxt;
           nxt = fetch(pbase + 32 + lane);
         }
-        if (i >= kStages && !mbar_wait_warp(empty_bar(s), ((i / kStages) - 1) & 1, abort_flag,
-                                            a.err, kErrTimeout, kWaitTimeoutNs))
+        if (!mbar_wait_warp(empty_bar(s), phase, abort_flag, a.err, kErrTimeout, kWaitTimeoutNs))
           break;
         // pages of this tile that hold a visible key
-        const int key = key0 + (lane & 3) * box;
-        const int pg = key >> page_log2;
-        const int page = __shfl_sync(0xffffffffu, cur.page, (pg - pbase) & 31);
-        const bool load = (lane & 3) < boxes && key < hi && key + box > lo;
-        const int n_load = __popc(__ballot_sync(0xffffffffu, load) & 0xFu);
+        const int key = key0 + sub * box;
+        const int page = __shfl_sync(0xffffffffu, cur.page, ((key >> page_log2) - pbase) & 31);
+        const bool load = sub < boxes && key < hi && key + box > lo;
+        const int n_load = __popc(__ballot_sync(0xffffffffu, load) & 0xFFu);
         if (kFp8) {
-          const int pw = (key0 + (lane & 3) * 16) >> page_log2;  // page of warp's 16 keys
+          const int pw = (key0 + sub * 16) >> page_log2;  // page of a block of 16 keys
           const float ks = __shfl_sync(0xffffffffu, cur.ks, (pw - pbase) & 31);
           const float vs = __shfl_sync(0xffffffffu, cur.vs, (pw - pbase) & 31);
-          if (lane < 4)
-            *reinterpret_cast<float4*>(smem + L::kPage + (s * kWarps + lane) * 16) =
+          if (lane < L::kPages)
+            *reinterpret_cast<float4*>(smem + L::kPage + (s * L::kPages + lane) * 16) =
                 page_factors(ks, vs);
           __syncwarp();
         }
@@ -182,10 +190,14 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
           mbar_arrive_expect_tx(full_bar(s),
                                 2u * static_cast<uint32_t>(n_load * box) * kRowBytes);
         __syncwarp();
-        if (load && lane < 8) {
-          const uint32_t dst = sbase + (lane < 4 ? L::kK : L::kV) + s * kTileBytes +
-                               static_cast<uint32_t>((lane & 3) * box) * kRowBytes;
-          tma_load_4d(dst, lane < 4 ? &maps.k : &maps.v, full_bar(s), 0, g, key & (P - 1), page);
+        if (load && lane < 16) {
+          const uint32_t dst = sbase + (lane < 8 ? L::kK : L::kV) + s * kTileBytes +
+                               static_cast<uint32_t>(sub * box) * kRowBytes;
+          tma_load_4d(dst, lane < 8 ? &maps.k : &maps.v, full_bar(s), 0, g, key & (P - 1), page);
+        }
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
         }
         issued = i + 1;
       }
@@ -296,78 +308,100 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
   // Keys that every token of the row sees need no mask.
   const int all_hi = idx0 + 1;  // keys below it are not past the first token
   const int all_lo = a.window > 0 ? min(idx0 + NT, len) - a.window : 0;
+  // this lane's places in a block of 16 keys
+  const uint32_t k_lane =
+      kFp8 ? gr * 64 + ((tc ^ ((gr >> 1) & 3)) << 4) : (lane & 15) * 128;
+  const int vr = kFp8 ? lane & 15 : (lane & 7) + 8 * (lane >> 4);  // key of a V matrix row
   bool ok = !skip;
+  int s = 0;
+  uint32_t phase = 0;
   for (int i = 0; ok && i < n_tiles; ++i) {
-    const int s = i % kStages;
-    if (!(ok = mbar_wait_warp(full_bar(s), (i / kStages) & 1, abort_flag, a.err, kErrTimeout,
-                              kWaitTimeoutNs)))
+    if (!(ok = mbar_wait_warp(full_bar(s), phase, abort_flag, a.err, kErrTimeout, kWaitTimeoutNs)))
       break;
-    const uint32_t sk = sbase + L::kK + s * kTileBytes + 16 * warp * kRowBytes;
-    const uint32_t sv = sbase + L::kV + s * kTileBytes + 16 * warp * kRowBytes;
-    const int key0 = key_a + i * kPagedTile + 16 * warp;
-    float4 pagef = make_float4(kScaleLog2, 0.f, 1.f, 0.f);
-    if (kFp8) pagef = *reinterpret_cast<const float4*>(smem + L::kPage + (s * kWarps + warp) * 16);
+    const uint32_t block0 = static_cast<uint32_t>(16 * kBlocks * warp);
+    const uint32_t sk = sbase + L::kK + s * kTileBytes + block0 * kRowBytes;
+    const uint32_t sv = sbase + L::kV + s * kTileBytes + block0 * kRowBytes;
+    const int key0 = key_a + i * kTile + static_cast<int>(block0);
+    float4 pagef[kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      pagef[u] = make_float4(kScaleLog2, 0.f, 1.f, 0.f);
+      if (kFp8)
+        pagef[u] = *reinterpret_cast<const float4*>(
+            smem + L::kPage + (s * L::kPages + kBlocks * warp + u) * 16);
+    }
 
-    // S^T: rows = keys gr and gr+8, columns = heads 2tc and 2tc+1
-    float sc[NT][4];
+    // S^T: rows = keys gr and gr+8 of a block, columns = heads 2tc and 2tc+1
+    float sc[kBlocks][NT][4];
 #pragma unroll
-    for (int tk = 0; tk < NT; ++tk) sc[tk][0] = sc[tk][1] = sc[tk][2] = sc[tk][3] = 0.f;
-    if (kFp8) {
-      const uint4 ka = lds128(sk + gr * 64 + ((tc ^ ((gr >> 1) & 3)) << 4));
-      const uint4 kb = lds128(sk + (gr + 8) * 64 + ((tc ^ ((gr >> 1) & 3)) << 4));
-      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+    for (int u = 0; u < kBlocks; ++u) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t f[4];
-        e4m3x4_to_f16(wa[kk], f[0], f[2]);
-        e4m3x4_to_f16(wb[kk], f[1], f[3]);
+      for (int tk = 0; tk < NT; ++tk) sc[u][tk][0] = sc[u][tk][1] = sc[u][tk][2] = sc[u][tk][3] = 0.f;
+      if (kFp8) {
+        const uint4 ka = lds128(sk + k_lane + u * 1024);
+        const uint4 kb = lds128(sk + k_lane + u * 1024 + 512);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int tk = 0; tk < NT; ++tk) mma_f16(sc[tk], f, qh[tk][kk][0], qh[tk][kk][1]);
-      }
-    } else {
-      const int r = (lane & 7) + 8 * ((lane >> 3) & 1);
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t f[4];
+          e4m3x4_to_f16(wa[kk], f[0], f[2]);
+          e4m3x4_to_f16(wb[kk], f[1], f[3]);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t f[4];
-        ldsm_x4(sk + r * 128 + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+          for (int tk = 0; tk < NT; ++tk) mma_f16(sc[u][tk], f, qh[tk][kk][0], qh[tk][kk][1]);
+        }
+      } else {
 #pragma unroll
-        for (int tk = 0; tk < NT; ++tk) {
-          mma_bf16(sc[tk], f, qh[tk][kk][0], qh[tk][kk][1]);
-          mma_bf16(sc[tk], f, ql[kFp8 ? 0 : tk][kk][0], ql[kFp8 ? 0 : tk][kk][1]);
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t f[4];
+          ldsm_x4(sk + k_lane + u * 2048 + (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4), f[0], f[1],
+                  f[2], f[3]);
+#pragma unroll
+          for (int tk = 0; tk < NT; ++tk) {
+            mma_bf16(sc[u][tk], f, qh[tk][kk][0], qh[tk][kk][1]);
+            mma_bf16(sc[u][tk], f, ql[kFp8 ? 0 : tk][kk][0], ql[kFp8 ? 0 : tk][kk][1]);
+          }
         }
       }
     }
 
     // Exponents x - m in log2 units; masked keys -inf.
-    const bool edge = key0 + 16 > all_hi || key0 < all_lo;
-    bool above = false;
-    float d[NT][4];
+    const bool edge = key0 + 16 * kBlocks > all_hi || key0 < all_lo;
+    float d[kBlocks][NT][4], top = -INFINITY;
 #pragma unroll
-    for (int tk = 0; tk < NT; ++tk) {
-      const float c0 = kFp8 ? pagef.x * qs[kFp8 ? tk : 0][0] : kScaleLog2;
-      const float c1 = kFp8 ? pagef.x * qs[kFp8 ? tk : 0][1] : kScaleLog2;
+    for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        d[tk][e] = fmaf(sc[tk][e], e & 1 ? c1 : c0, pagef.y - m[tk][e & 1]);
-      if (edge) {
-        const int top = idx0 + tk, k0 = key0 + gr, k1 = k0 + 8;
-        const int low = a.window > 0 ? top - a.window : -1;
-        if (k0 > top || k0 <= low) d[tk][0] = d[tk][1] = -INFINITY;
-        if (k1 > top || k1 <= low) d[tk][2] = d[tk][3] = -INFINITY;
+      for (int tk = 0; tk < NT; ++tk) {
+        const float c0 = kFp8 ? pagef[u].x * qs[kFp8 ? tk : 0][0] : kScaleLog2;
+        const float c1 = kFp8 ? pagef[u].x * qs[kFp8 ? tk : 0][1] : kScaleLog2;
+        const float y0 = pagef[u].y - m[tk][0], y1 = pagef[u].y - m[tk][1];
+        d[u][tk][0] = fmaf(sc[u][tk][0], c0, y0);
+        d[u][tk][1] = fmaf(sc[u][tk][1], c1, y1);
+        d[u][tk][2] = fmaf(sc[u][tk][2], c0, y0);
+        d[u][tk][3] = fmaf(sc[u][tk][3], c1, y1);
+        if (edge) {
+          const int last = idx0 + tk, k0 = key0 + 16 * u + gr, k1 = k0 + 8;
+          const int before = a.window > 0 ? last - a.window : -1;
+          if (k0 > last || k0 <= before) d[u][tk][0] = d[u][tk][1] = -INFINITY;
+          if (k1 > last || k1 <= before) d[u][tk][2] = d[u][tk][3] = -INFINITY;
+        }
+        top = fmax3(top, fmaxf(d[u][tk][0], d[u][tk][1]), fmaxf(d[u][tk][2], d[u][tk][3]));
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) above = above || d[tk][e] > kRescaleThreshold;
-    }
-    if (__any_sync(0xffffffffu, above)) {
-      // new maxima of every head, over the warp's 16 keys
+    if (__any_sync(0xffffffffu, top > kRescaleThreshold)) {
+      // new maxima of every head, over the warp's keys
 #pragma unroll
       for (int tk = 0; tk < NT; ++tk) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float c = kFp8 ? pagef.x * qs[kFp8 ? tk : 0][h] : kScaleLog2;
-          const float x0 = d[tk][h] == -INFINITY ? kNoMax : fmaf(sc[tk][h], c, pagef.y);
-          const float x1 = d[tk][2 + h] == -INFINITY ? kNoMax : fmaf(sc[tk][2 + h], c, pagef.y);
-          float mx = fmaxf(m[tk][h], fmaxf(x0, x1));
+          float x[kBlocks][2], mx = m[tk][h];
+#pragma unroll
+          for (int u = 0; u < kBlocks; ++u) {
+            const float c = kFp8 ? pagef[u].x * qs[kFp8 ? tk : 0][h] : kScaleLog2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              x[u][e] = fmaf(sc[u][tk][2 * e + h], c, pagef[u].y);
+              if (d[u][tk][2 * e + h] != -INFINITY) mx = fmaxf(mx, x[u][e]);
+            }
+          }
 #pragma unroll
           for (int w = 4; w < 32; w *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
           const float alpha = ex2_approx(m[tk][h] - mx);
@@ -378,93 +412,100 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : kFp8 ? 5 : 4)
             o[tk][mt][h] *= alpha;
             o[tk][mt][2 + h] *= alpha;
           }
-          if (d[tk][h] != -INFINITY) d[tk][h] = x0 - mx;
-          if (d[tk][2 + h] != -INFINITY) d[tk][2 + h] = x1 - mx;
+#pragma unroll
+          for (int u = 0; u < kBlocks; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (d[u][tk][2 * e + h] != -INFINITY) d[u][tk][2 * e + h] = x[u][e] - mx;
         }
       }
     }
 
     // P^T, transposed to the B operand (row = key, column = head)
-    uint32_t ph[NT][2], pl[kFp8 ? 1 : NT][2];
+    uint32_t ph[kBlocks][NT][2], pl[kBlocks][kFp8 ? 1 : NT][2];
 #pragma unroll
-    for (int tk = 0; tk < NT; ++tk) {
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = ex2_approx(d[tk][e]);
-      l[tk][0] = fmaf(p[0] + p[2], pagef.z, l[tk][0]);
-      l[tk][1] = fmaf(p[1] + p[3], pagef.z, l[tk][1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (kFp8) {
-          ph[tk][h] = transpose8(pack_f16x2(p[2 * h], p[2 * h + 1]));
-        } else {
-          const uint32_t w = pack_bf16x2(p[2 * h], p[2 * h + 1]);
-          ph[tk][h] = transpose8(w);
-          pl[kFp8 ? 0 : tk][h] = transpose8(
-              pack_bf16x2(p[2 * h] - bf16lo_to_f32(w), p[2 * h + 1] - bf16hi_to_f32(w)));
-        }
-      }
-    }
-
-    // O^T += V^T P^T. On an edge the values of a token's masked keys are zeroed:
-    // their p is 0, but what lies there may be infinite or NaN.
-    auto accumulate = [&](int mt, const uint32_t (&f)[4]) {
+    for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
       for (int tk = 0; tk < NT; ++tk) {
-        if (edge) {
-          const int top = idx0 + tk, low = a.window > 0 ? top - a.window : -1;
-          uint32_t z[4];
+        float p[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k0 = key0 + 8 * h + 2 * tc;
-            const uint32_t keep = (k0 <= top && k0 > low ? 0x0000FFFFu : 0u) |
-                                  (k0 + 1 <= top && k0 + 1 > low ? 0xFFFF0000u : 0u);
-            z[2 * h] = f[2 * h] & keep;
-            z[2 * h + 1] = f[2 * h + 1] & keep;
+        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(d[u][tk][e]);
+        l[tk][0] = fmaf(p[0] + p[2], pagef[u].z, l[tk][0]);
+        l[tk][1] = fmaf(p[1] + p[3], pagef[u].z, l[tk][1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (kFp8) {
+            ph[u][tk][h] = transpose8(pack_f16x2(p[2 * h], p[2 * h + 1]));
+          } else {
+            const uint32_t w = pack_bf16x2(p[2 * h], p[2 * h + 1]);
+            ph[u][tk][h] = transpose8(w);
+            pl[u][kFp8 ? 0 : tk][h] = transpose8(
+                pack_bf16x2(p[2 * h] - bf16lo_to_f32(w), p[2 * h + 1] - bf16hi_to_f32(w)));
+          }
+        }
+      }
+
+    // O^T += V^T P^T
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      auto accumulate = [&](int mt, const uint32_t (&f)[4]) {
+#pragma unroll
+        for (int tk = 0; tk < NT; ++tk) {
+          uint32_t z[4] = {f[0], f[1], f[2], f[3]};
+          if (edge) {
+            // the values of this token's masked keys are zeroed: their p is 0, but what lies
+            // there may be infinite or NaN
+            const int last = idx0 + tk, before = a.window > 0 ? last - a.window : -1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k0 = key0 + 16 * u + 8 * h + 2 * tc;
+              const uint32_t keep = (k0 <= last && k0 > before ? 0x0000FFFFu : 0u) |
+                                    (k0 + 1 <= last && k0 + 1 > before ? 0xFFFF0000u : 0u);
+              z[2 * h] &= keep;
+              z[2 * h + 1] &= keep;
+            }
           }
           if (kFp8) {
-            mma_f16(o[tk][mt], z, ph[tk][0], ph[tk][1]);
+            mma_f16(o[tk][mt], z, ph[u][tk][0], ph[u][tk][1]);
           } else {
-            mma_bf16(o[tk][mt], z, ph[tk][0], ph[tk][1]);
-            mma_bf16(o[tk][mt], z, pl[kFp8 ? 0 : tk][0], pl[kFp8 ? 0 : tk][1]);
+            mma_bf16(o[tk][mt], z, ph[u][tk][0], ph[u][tk][1]);
+            mma_bf16(o[tk][mt], z, pl[u][kFp8 ? 0 : tk][0], pl[u][kFp8 ? 0 : tk][1]);
           }
-        } else if (kFp8) {
-          mma_f16(o[tk][mt], f, ph[tk][0], ph[tk][1]);
-        } else {
-          mma_bf16(o[tk][mt], f, ph[tk][0], ph[tk][1]);
-          mma_bf16(o[tk][mt], f, pl[kFp8 ? 0 : tk][0], pl[kFp8 ? 0 : tk][1]);
         }
-      }
-    };
-    if (kFp8) {
-      // a lane's word: keys 2tc, 2tc+1 of elements 16c+2gr, 16c+2gr+1; rows gr and
-      // gr+8 of tile c stand for those two
-      const int r = (lane & 7) + 8 * ((lane >> 3) & 1);
+      };
+      if (kFp8) {
+        // a lane's word: keys 2tc, 2tc+1 of elements 16c+2gr, 16c+2gr+1; rows gr and
+        // gr+8 of tile c stand for those two
 #pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t w[4];
-        ldsm_x4_trans(sv + r * 64 + (((c + (lane >> 4)) ^ ((r >> 1) & 3)) << 4), w[0], w[1], w[2],
-                      w[3]);
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t w[4];
+          ldsm_x4_trans(sv + u * 1024 + vr * 64 + (((c + (lane >> 4)) ^ ((vr >> 1) & 3)) << 4), w[0],
+                        w[1], w[2], w[3]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+          for (int v = 0; v < 2; ++v) {
+            uint32_t f[4];
+            e4m3x4_to_f16(__byte_perm(w[2 * v], 0, 0x3120), f[0], f[1]);
+            e4m3x4_to_f16(__byte_perm(w[2 * v + 1], 0, 0x3120), f[2], f[3]);
+            accumulate(c + v, f);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
           uint32_t f[4];
-          e4m3x4_to_f16(__byte_perm(w[2 * u], 0, 0x3120), f[0], f[1]);
-          e4m3x4_to_f16(__byte_perm(w[2 * u + 1], 0, 0x3120), f[2], f[3]);
-          accumulate(c + u, f);
+          ldsm_x4_trans(
+              sv + u * 2048 + vr * 128 + (((2 * mt + ((lane >> 3) & 1)) ^ (vr & 7)) << 4), f[0],
+              f[1], f[2], f[3]);
+          accumulate(mt, f);
         }
-      }
-    } else {
-      const int r = (lane & 7) + 8 * (lane >> 4);
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        uint32_t f[4];
-        ldsm_x4_trans(sv + r * 128 + (((2 * mt + ((lane >> 3) & 1)) ^ (r & 7)) << 4), f[0], f[1],
-                      f[2], f[3]);
-        accumulate(mt, f);
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty_bar(s));
+    if (++s == kStages) {
+      s = 0;
+      phase ^= 1;
+    }
   }
 
   // ---- join the warps
@@ -549,7 +590,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  const int most = paged_most_tiles(a.n, a.max_len, a.window);
+  const int most = paged_most_tiles(NT, Shape<kFp8>::kTile, a.max_len, a.window);
   const int64_t chunks = paged_max_chunks(a.rows, most, a.target);
   cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
   cfg.blockDim = dim3(kThreads);

@@ -118,9 +118,7 @@ int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
 // Eight CTAs, one per kv head, make a chunk.
 int paged_target(int n) { return (paged_row_tokens(n) <= 2 ? 148 * 3 * 4 : 148 * 2) / kNumKvHeads; }
 
-int paged_most_tiles(int n, int max_len, int window) {
-  const int nt = paged_row_tokens(n);
-  const int tile = nt <= 2 ? kPagedTile : kPagedTileN;
+int paged_most_tiles(int nt, int tile, int max_len, int window) {
   // a row of nt tokens sees window + nt - 1 keys, from anywhere in a tile
   return paged_row_tiles(0, window > 0 && window + nt + tile < max_len ? window + nt + tile : max_len,
                          tile);
@@ -132,7 +130,10 @@ size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_
   off[0] = 0;
   off[1] = parts * kHeadDim * sizeof(float);
   off[2] = off[1] + parts * sizeof(float2);
-  if (paged_most_tiles(n, max_len, window) <= kPagedWhole) return 0;
+  // (the kernel for few tokens takes longer tiles of e4m3 pages, and cuts them less)
+  const int nt = paged_row_tokens(n);
+  const int most = paged_most_tiles(nt, nt <= 2 ? kPagedTile : kPagedTileN, max_len, window);
+  if (most <= kPagedWhole) return 0;
   return off[2] + ((static_cast<size_t>(rows) * sizeof(int2) + 15) & ~static_cast<size_t>(15));
 }
 

@@ -701,7 +701,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  const int most = paged_most_tiles(a.n, a.max_len, a.window);
+  const int most = paged_most_tiles(kNT, kTile, a.max_len, a.window);
   const int64_t chunks = paged_max_chunks(a.rows, most, a.target);
   cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
   cfg.blockDim = dim3(kThreads);
