@@ -114,9 +114,14 @@ cudaError_t launch_paged_combine(const PagedAttentionArgs& a, int row_tokens, cu
 
 int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
 
-// Few tokens: about four waves of three CTAs per SM; many: one wave of two CTAs.
-// Eight CTAs, one per kv head, make a chunk.
-int paged_target(int n) { return (paged_row_tokens(n) <= 2 ? 148 * 3 * 4 : 148 * 2) / kNumKvHeads; }
+// Eight CTAs, one per kv head, make a chunk. Few tokens: about four waves of three CTAs
+// per SM. Many: one wave of two; a row's last chunk is half empty on average, so that
+// many rows' chunks are made longer.
+int paged_target(int n, int64_t rows) {
+  if (paged_row_tokens(n) <= 2) return 148 * 3 * 4 / kNumKvHeads;
+  const int wave = 148 * 2 / kNumKvHeads;
+  return rows < wave ? wave - static_cast<int>(rows / 2) : wave;
+}
 
 int paged_most_tiles(int nt, int tile, int max_len, int window) {
   // a row of nt tokens sees window + nt - 1 keys, from anywhere in a tile
@@ -125,7 +130,7 @@ int paged_most_tiles(int nt, int tile, int max_len, int window) {
 }
 
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]) {
-  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(n))) * kNumKvHeads *
+  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(n, 0))) * kNumKvHeads *
                        paged_row_tokens(n) * kGroup;
   off[0] = 0;
   off[1] = parts * kHeadDim * sizeof(float);

@@ -6,13 +6,15 @@
 // tensor memory. Work is cut as for few tokens (paged.h): rows by tiles of 128 keys,
 // rows of many tiles into chunks that the combine kernel joins.
 //
-// Two CTAs per SM, each with one row: one's softmax runs while the other's products
-// and loads do, with no hand-over between them. Roles (256 threads):
+// A CTA has two halves of 256 threads, which take two kv heads of the same chunk, each
+// with its own pipeline. Their softmax warps take turns at the exponential unit: left
+// alone (as two CTAs of an SM) they fall into step, use it together and then leave it
+// idle together. Roles in a half:
 //   warps 0-3  softmax, one thread per query row (TMEM lane): rotate and store Q, then
 //              per tile load S (128 columns), exponentials, P to TMEM; at the end O.
 //              Warps whose four tokens are past the row's last take no part.
 //   warp 4     producer: pages to shared memory (TMA)
-//   warp 5     issues the products, owns the tensor memory
+//   warp 5     issues the products (of the first half: owns the tensor memory)
 //   warps 6-7  e4m3: codes to f16, K and V of a tile each into its own buffer
 //
 // Precision. bf16 pages: q in two bf16 terms (two products), p in one (2^-8). e4m3
@@ -34,20 +36,26 @@ namespace {
 
 constexpr int kNT = kPagedManyTokens;
 constexpr int kTile = kPagedTileN;
-constexpr int kThreads = 256;
-constexpr uint32_t kTmemCols = 256;  // S [0,128), P [128,192), O [192,256); two CTAs per SM
+constexpr int kHalf = 256;  // threads of a half
+constexpr int kThreads = 2 * kHalf;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kHalfCols = 256;  // S [0,128), P [128,192), O [192,256)
 constexpr uint32_t kColP = 128, kColO = 192;
 constexpr uint32_t kTile16 = kTile * kHeadDim * 2;  // a tile of 16-bit elements
 constexpr uint32_t kTile8 = kTile * kHeadDim;
 
 constexpr uint32_t kRegsLight = 72;
 constexpr uint32_t kRegsSoftmax = 184;
-static_assert(128 * kRegsLight + 128 * kRegsSoftmax <= 256 * 128, "register split");
+static_assert(256 * kRegsLight + 256 * kRegsSoftmax <= 512 * 128, "register split");
+
+// Exp-loop step (of 64 column pairs) at which a softmax warp lets the other half's go on.
+constexpr int kTurnHandOff = 38;
 
 constexpr int kRaw = 3;    // stages of e4m3 tiles
 constexpr int kPageRing = 4;  // tiles whose pages' factors are held: written by the producer up
                               // to kRaw tiles ahead of the softmax
 
+// A half's shared memory; then what the CTA shares.
 template <bool kFp8>
 struct Smem {
   static constexpr int kStages = kFp8 ? 1 : 2;  // of the 16-bit operands
@@ -58,13 +66,13 @@ struct Smem {
   static constexpr uint32_t kRawV = kRawK + (kFp8 ? kRaw : 0) * kTile8;
   static constexpr uint32_t kPage = kRawV + (kFp8 ? kRaw : 0) * kTile8;  // float4 [ring][8]
   static constexpr uint32_t kBar = kPage + (kFp8 ? kPageRing * 8 * 16 : 0);
-  static constexpr uint32_t kScan = kBar + 24 * 8;  // 8 + 8 warp sums, slot
-  static constexpr uint32_t kMisc = kScan + 16 * 8 + 16;  // abort flag, TMEM address
-  static constexpr uint32_t kBad = kMisc + 16;            // [2][4] value rows taken out of a tile
-  static constexpr uint32_t kBytes = kBad + 32 + 1024;
+  static constexpr uint32_t kBad = kBar + 32 * 8;  // [2][4] value rows taken out of a tile
+  static constexpr uint32_t kHalfBytes = (kBad + 32 + 1023) / 1024 * 1024;
+  static constexpr uint32_t kScan = 2 * kHalfBytes;  // 16 + 16 warp sums, slot
+  static constexpr uint32_t kMisc = kScan + 32 * 8 + 16;  // abort flag, TMEM address
+  static constexpr uint32_t kBytes = kMisc + 16 + 1024;
 };
-static_assert(2 * (Smem<false>::kBytes + 1024) <= 228 * 1024 &&
-              2 * (Smem<true>::kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(Smem<false>::kBytes <= 227 * 1024 && Smem<true>::kBytes <= 227 * 1024, "shared memory");
 
 enum : int {
   BAR_Q = 0,        // Q stored and O zeroed
@@ -80,9 +88,10 @@ enum : int {
   BAR_RAW = BAR_V_FREE + 2,     // [kRaw] e4m3: tile loaded
   BAR_RAW_FREE = BAR_RAW + kRaw,
   BAR_EDGE = BAR_RAW_FREE + kRaw,  // [2] softmax warps' steps in a tile at the edge
-  NUM_BARS = BAR_EDGE + 2
+  BAR_TURN = BAR_EDGE + 2,         // [4] softmax warp w may use the exponential unit
+  NUM_BARS = BAR_TURN + 4
 };
-static_assert(NUM_BARS <= 24, "barriers");
+static_assert(NUM_BARS <= 32, "barriers");
 
 // Instruction descriptor, kind::f16, fp32 accumulators.
 template <bool kFp8>
@@ -165,7 +174,7 @@ __device__ __forceinline__ float store_query(const PagedAttentionArgs& a, uint8_
     f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     unit = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   }
-  uint8_t* row = smem + Smem<kFp8>::kQ + r * 128;
+  uint8_t* row = smem + Smem<kFp8>::kQ + r * 128;  // of this half
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t w[4], v[4];
@@ -187,7 +196,7 @@ __device__ __forceinline__ float store_query(const PagedAttentionArgs& a, uint8_
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedMaps maps, const PagedAttentionArgs a) {
   using L = Smem<kFp8>;
   constexpr uint32_t kRowBytes = kHeadDim * (kFp8 ? 1 : 2);
@@ -195,24 +204,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
+  const int half = static_cast<int>(threadIdx.x / kHalf);
+  uint8_t* cta_smem = smem;
+  smem += half * L::kHalfBytes;  // this half's
   Ctx ctx;
   ctx.sbase = smem_u32(smem);
   ctx.bars = ctx.sbase + L::kBar;
-  ctx.abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
+  ctx.abort_flag = reinterpret_cast<volatile int*>(cta_smem + L::kMisc);
   ctx.err = a.err;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc + 4);
-  const int warp = static_cast<int>(threadIdx.x >> 5);
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  const int g = static_cast<int>(blockIdx.x % kNumKvHeads);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cta_smem + L::kMisc + 4);
+  const int ht = static_cast<int>(threadIdx.x % kHalf);  // thread and warp of the half
+  const int warp = ht >> 5;
+  const int lane = ht & 31;
+  constexpr int kCtas = kNumKvHeads / 2;  // of a chunk
+  const int g = static_cast<int>(blockIdx.x % kCtas) * 2 + half;
 
   // The tokens, lengths and pages, the workspace and the tensor memory may still be in
   // use by the kernel before.
   griddep_wait();
   if (threadIdx.x == 0)
     *ctx.abort_flag = (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) ? 1 : 0;
-  ScanSlot* slot = reinterpret_cast<ScanSlot*>(smem + L::kScan + 16 * 8);
-  if (!find_chunk<kNT, kTile, kThreads>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
-                                        reinterpret_cast<uint64_t*>(smem + L::kScan), slot))
+  ScanSlot* slot = reinterpret_cast<ScanSlot*>(cta_smem + L::kScan + 32 * 8);
+  if (!find_chunk<kNT, kTile, kThreads>(a, static_cast<int>(blockIdx.x / kCtas),
+                                        reinterpret_cast<uint64_t*>(cta_smem + L::kScan), slot))
     return;  // past the call's last chunk
   const bool skip = *ctx.abort_flag != 0;
   const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
@@ -231,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int page_log2 = a.cache.page_log2;
   const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
 
-  if (threadIdx.x == 0) {
+  if (ht == 0) {
     const uint32_t warps = static_cast<uint32_t>(active);
     mbar_init(ctx.bar(BAR_Q), 32 * warps);
     mbar_init(ctx.bar(BAR_S_FULL), 1);
@@ -247,20 +261,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     mbar_init(ctx.bar(BAR_EDGE), warps);
     mbar_init(ctx.bar(BAR_EDGE + 1), warps);
+    for (int i = 0; i < 4; ++i) mbar_init(ctx.bar(BAR_TURN + i), 1);
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(ctx.bar(BAR_RAW + i), 1);
       mbar_init(ctx.bar(BAR_RAW_FREE + i), 64);
     }
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (half == 0 && warp == 5) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot + half * kHalfCols;
 
   if (warp >= 4) {
     setmaxnreg_dec<kRegsLight>();
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_wait(ctx.bar(BAR_DONE), 0, &never, nullptr, 0, kWaitTimeoutNs);
     } else if (kFp8 && warp >= 6 && !skip) {
       // ---------------------------------------------------------------- e4m3 to f16
-      const int t = static_cast<int>(threadIdx.x) - 192;  // 0..63
+      const int t = ht - 192;  // 0..63
       // one tile of codes (64-byte rows, 64-byte swizzle) to f16 (128-byte rows and swizzle)
       auto convert = [&](uint32_t src, uint32_t dst) {
 #pragma unroll 2
@@ -406,22 +421,28 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         fence_async_smem();
       };
-      for (int j = 0; j < n_tiles; ++j) {
+      // K of tile j+1 before V of tile j: Q K^T runs a tile ahead of P V
+      auto convert_k = [&](int j) {
         const int s = j % kRaw;
-        if (!ctx.wait_warp(BAR_RAW + s, (j / kRaw) & 1)) break;
-        if (j > 0 && !ctx.wait_warp(BAR_S_FULL, (j - 1) & 1)) break;  // K of tile j-1 is free
+        if (!ctx.wait_warp(BAR_RAW + s, (j / kRaw) & 1)) return false;
+        if (j > 0 && !ctx.wait_warp(BAR_S_FULL, (j - 1) & 1)) return false;  // the one before is used
         convert(ctx.sbase + L::kRawK + s * kTile8, ctx.sbase + L::kK);
         mbar_arrive(ctx.bar(BAR_K_FULL));
-        if (j > 0 && !ctx.wait_warp(BAR_PV, (j - 1) & 1)) break;      // and its V
-        convert(ctx.sbase + L::kRawV + s * kTile8, ctx.sbase + L::kV);
+        return true;
+      };
+      bool ok = n_tiles > 0 && convert_k(0);
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        if (j + 1 < n_tiles && !(ok = convert_k(j + 1))) break;
+        if (j > 0 && !(ok = ctx.wait_warp(BAR_PV, (j - 1) & 1))) break;  // V of the one before is used
+        convert(ctx.sbase + L::kRawV + (j % kRaw) * kTile8, ctx.sbase + L::kV);
         mbar_arrive(ctx.bar(BAR_V_FULL));
-        mbar_arrive(ctx.bar(BAR_RAW_FREE + s));
+        mbar_arrive(ctx.bar(BAR_RAW_FREE + j % kRaw));
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax
     setmaxnreg_inc<kRegsSoftmax>();
-    const int r = static_cast<int>(threadIdx.x);  // row = TMEM lane
+    const int r = ht;  // row = TMEM lane
     if (warp < active && !skip) {
       const int t = t0 + (r >> 3);       // token
       const int idx = idx0 + (r >> 3);   // its index
@@ -445,6 +466,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int edge_lo = a.window > 0 ? min(idx0 + kNT, len) - a.window : 0;
       const int edge_hi = idx0 + 1;
       const int first = a.window > 0 ? idx - a.window + 1 : 0;  // this row sees [first, idx]
+      // the other half's barrier for this warp
+      const uint32_t other_turn = ctx.bar(BAR_TURN + warp) +
+                                  (half ? 0u - L::kHalfBytes : L::kHalfBytes);
       uint32_t edges = 0;  // tiles at the edge so far
       // all softmax warps meet; a wait like the others, so that none waits for ever
       auto meet = [&](int step) {
@@ -506,6 +530,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           l *= alpha;
           m = mx;
         }
+        // The halves' warps of a scheduler take turns: half 0 tile j, half 1 tile j, half 0
+        // tile j+1, ...
+        if ((j > 0 || half == 1) && !(ok = ctx.wait_warp(BAR_TURN + warp, (half ? j : j - 1) & 1)))
+          break;
         // P and the sums' terms; a thread's 128 exponentials, packed in place
         const uint64_t c2 = f2_pack(kScaleLog2, kScaleLog2);
         const uint64_t nm2 = f2_pack(-m, -m);
@@ -523,6 +551,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           acc1 = fadd2(acc1, f2_pack(p2, p3));
           sv[i] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           sv[i + 1] = kFp8 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
+          if (i == kTurnHandOff) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(other_turn);
+          }
           if (kFp8 && i % 8 == 6) {  // the end of a page's 16 columns
             float s0, s1, s2, s3;
             f2_unpack(acc0, s0, s1);
@@ -681,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 5) {
+  if (half == 0 && warp == 5) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -703,7 +735,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStrea
   cfg.stream = stream;
   const int most = paged_most_tiles(kNT, kTile, a.max_len, a.window);
   const int64_t chunks = paged_max_chunks(a.rows, most, a.target);
-  cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
+  cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads / 2));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   e = cudaLaunchKernelEx(&cfg, paged_many_kernel<kFp8>, maps, a);
