@@ -61,7 +61,7 @@ struct Smem {
   static constexpr uint32_t kPage = kQExp + NT * kGroup * 4;
   static constexpr uint32_t kBar = kPage + Shape<kFp8>::kStages * kPages * 16;
   static constexpr uint32_t kScan = kBar + 2 * Shape<kFp8>::kStages * 8;  // 5 + 5 warp sums, slot
-  static constexpr uint32_t kMisc = kScan + 2 * 5 * 8 + 16;
+  static constexpr uint32_t kMisc = kScan + 2 * 5 * 8 + sizeof(ScanSlot);
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
 };
 
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : 4)
     a.meta[row] = make_int2(slot->part, chunks);
   const int b = row / a.groups;
   const int t0 = (row - b * a.groups) * NT;
-  const int len = min(max(__ldg(a.len + b), 0), a.max_len);
+  const int len = slot->len;
   const int idx0 = len - a.n + t0;  // index of the row's first token
   int lo, hi, tile_a, tile_b;
   paged_row_range(len, a.n, t0, NT, a.window, &lo, &hi);

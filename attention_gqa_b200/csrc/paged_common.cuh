@@ -36,7 +36,7 @@ inline cudaError_t allow_shared(const void* kernel, uint32_t bytes, std::atomic<
 }
 
 struct ScanSlot {
-  int row, split, chunks, part;
+  int row, split, chunks, part, len, unused;
 };
 
 // Length of sequence b, clamped to the table; one outside it is reported.
@@ -113,6 +113,7 @@ __device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid,
         slot->split = i;
         slot->chunks = n;
         slot->part = static_cast<int>(at >> 32);
+        slot->len = min(max(__ldg(a.len + r / a.groups), 0), a.max_len);
         break;
       }
       at += static_cast<uint64_t>(n) | (n > 1 ? static_cast<uint64_t>(n) << 32 : 0);

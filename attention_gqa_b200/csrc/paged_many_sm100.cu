@@ -15,7 +15,8 @@
 //              Warps whose four tokens are past the row's last take no part.
 //   warp 4     producer: pages to shared memory (TMA)
 //   warp 5     issues the products (of the first half: owns the tensor memory)
-//   warps 6-7  e4m3: codes to f16, K and V of a tile each into its own buffer
+//   warps 6-7  look over the value rows of tiles at the edge; e4m3: codes to f16, K and V
+//              of a tile each into its own buffer
 //
 // Precision. bf16 pages: q in two bf16 terms (two products), p in one (2^-8). e4m3
 // pages: codes are exact in f16, and q, scaled by a power of two, and p are f16 (2^-12
@@ -24,8 +25,8 @@
 // Masked values. P is 0 where a query does not see a key, but 0 * NaN is NaN, and in a
 // tile at the edge of what is visible the value rows may be stale or belong to later
 // tokens. There, value rows that no token of the row sees, or that hold an infinity
-// or NaN, are zeroed in shared memory; the latter are added to the queries that see them
-// one by one (exact, and as slow as it is rare).
+// or NaN, are zeroed in shared memory; the latter are noted, and the softmax warps add
+// them to the queries that see them one by one (exact, and as slow as it is rare).
 //
 // Bound by the exponential unit for whole rows: 128 x 128 of them per tile take 1024
 // cycles of an SM.
@@ -69,7 +70,7 @@ struct Smem {
   static constexpr uint32_t kBad = kBar + 32 * 8;  // [2][4] value rows taken out of a tile
   static constexpr uint32_t kHalfBytes = (kBad + 32 + 1023) / 1024 * 1024;
   static constexpr uint32_t kScan = 2 * kHalfBytes;  // 16 + 16 warp sums, slot
-  static constexpr uint32_t kMisc = kScan + 32 * 8 + 16;  // abort flag, TMEM address
+  static constexpr uint32_t kMisc = kScan + 32 * 8 + sizeof(ScanSlot);  // abort flag, TMEM address
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
 };
 static_assert(Smem<false>::kBytes <= 227 * 1024 && Smem<true>::kBytes <= 227 * 1024, "shared memory");
@@ -87,8 +88,8 @@ enum : int {
   BAR_V_FREE = BAR_K_FREE + 2,
   BAR_RAW = BAR_V_FREE + 2,     // [kRaw] e4m3: tile loaded
   BAR_RAW_FREE = BAR_RAW + kRaw,
-  BAR_EDGE = BAR_RAW_FREE + kRaw,  // [2] softmax warps' steps in a tile at the edge
-  BAR_TURN = BAR_EDGE + 2,         // [4] softmax warp w may use the exponential unit
+  BAR_SEEN = BAR_RAW_FREE + kRaw,  // [2] value rows of a tile at the edge looked over
+  BAR_TURN = BAR_SEEN + 2,         // [4] softmax warp w may use the exponential unit
   NUM_BARS = BAR_TURN + 4
 };
 static_assert(NUM_BARS <= 32, "barriers");
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     a.meta[row] = make_int2(slot->part, chunks);
   const int b = row / a.groups;
   const int t0 = (row - b * a.groups) * kNT;
-  const int len = min(max(__ldg(a.len + b), 0), a.max_len);
+  const int len = slot->len;
   const int idx0 = len - a.n + t0;  // index of the row's first token
   int lo, hi, tile_a, tile_b;
   paged_row_range(len, a.n, t0, kNT, a.window, &lo, &hi);
@@ -245,40 +246,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int page_log2 = a.cache.page_log2;
   const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
 
-  if (ht == 0) {
-    const uint32_t warps = static_cast<uint32_t>(active);
-    mbar_init(ctx.bar(BAR_Q), 32 * warps);
-    mbar_init(ctx.bar(BAR_S_FULL), 1);
-    mbar_init(ctx.bar(BAR_S_FREE), warps);
-    mbar_init(ctx.bar(BAR_P_FULL), warps);
-    mbar_init(ctx.bar(BAR_PV), 1);
-    mbar_init(ctx.bar(BAR_DONE), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(ctx.bar(BAR_K_FULL + i), kFp8 ? 64 : 1);
-      mbar_init(ctx.bar(BAR_V_FULL + i), kFp8 ? 64 : 1);
-      mbar_init(ctx.bar(BAR_K_FREE + i), 1);
-      mbar_init(ctx.bar(BAR_V_FREE + i), 1);
-    }
-    mbar_init(ctx.bar(BAR_EDGE), warps);
-    mbar_init(ctx.bar(BAR_EDGE + 1), warps);
-    for (int i = 0; i < 4; ++i) mbar_init(ctx.bar(BAR_TURN + i), 1);
-    for (int i = 0; i < kRaw; ++i) {
-      mbar_init(ctx.bar(BAR_RAW + i), 1);
-      mbar_init(ctx.bar(BAR_RAW_FREE + i), 64);
-    }
-    fence_barrier_init();
-  }
-  if (half == 0 && warp == 5) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot + half * kHalfCols;
+  // Keys from edge_hi on, or below edge_lo, are masked for some token of the row.
+  const int edge_lo = a.window > 0 ? min(idx0 + kNT, len) - a.window : 0;
+  const int edge_hi = idx0 + 1;
+  auto at_edge = [&](int j) {
+    const int key0 = key_a + j * kTile;
+    return key0 + kTile > edge_hi || key0 < edge_lo;
+  };
 
   if (warp >= 4) {
     setmaxnreg_dec<kRegsLight>();
+    // Barriers and tensor memory, for these warps now and for the softmax warps (barrier 1)
+    // when they have stored Q.
+    if (ht == kHalf / 2) {
+      const uint32_t warps = static_cast<uint32_t>(active);
+      mbar_init(ctx.bar(BAR_Q), 32 * warps);
+      mbar_init(ctx.bar(BAR_S_FULL), 1);
+      mbar_init(ctx.bar(BAR_S_FREE), warps);
+      mbar_init(ctx.bar(BAR_P_FULL), warps);
+      mbar_init(ctx.bar(BAR_PV), 1);
+      mbar_init(ctx.bar(BAR_DONE), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(ctx.bar(BAR_K_FULL + i), kFp8 ? 64 : 1);
+        mbar_init(ctx.bar(BAR_V_FULL + i), kFp8 ? 64 : 1);
+        mbar_init(ctx.bar(BAR_K_FREE + i), 1);
+        mbar_init(ctx.bar(BAR_V_FREE + i), 3);  // the products, warps 6 and 7
+        mbar_init(ctx.bar(BAR_SEEN + i), 64);
+      }
+      for (int i = 0; i < 4; ++i) mbar_init(ctx.bar(BAR_TURN + i), 1);
+      for (int i = 0; i < kRaw; ++i) {
+        mbar_init(ctx.bar(BAR_RAW + i), 1);
+        mbar_init(ctx.bar(BAR_RAW_FREE + i), 64);
+      }
+      fence_barrier_init();
+    }
+    if (half == 0 && warp == 5) {
+      tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+      tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    named_barrier(2, kThreads / 2);
+    tc_fence_after_sync();
+    named_arrive(1, kThreads);
+    const uint32_t tmem = *tmem_slot + half * kHalfCols;
     if (warp == 4 && !skip) {
       // ---------------------------------------------------------------- producer
       if (lane == 0) {
@@ -382,10 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kFp8) mma_commit(ctx.bar(BAR_K_FREE + s));
         return true;
       };
+      uint32_t edges = 0;  // tiles at the edge so far
       auto issue_pv = [&](int j) {
         const int s = kFp8 ? 0 : j & 1;
         if (!ctx.wait(BAR_V_FULL + s, (kFp8 ? j : j >> 1) & 1) || !ctx.wait(BAR_P_FULL, j & 1))
           return false;
+        if (!kFp8 && at_edge(j)) {
+          if (!ctx.wait(BAR_SEEN + (edges & 1), (edges >> 1) & 1)) return false;
+          ++edges;
+        }
         tc_fence_after_sync();
         const uint64_t va = sdesc_sw128(ctx.sbase + L::kV + s * kTile16);
 #pragma unroll
@@ -402,11 +417,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(ctx.bar(BAR_DONE));
       volatile int never = 0;
       mbar_wait(ctx.bar(BAR_DONE), 0, &never, nullptr, 0, kWaitTimeoutNs);
-    } else if (kFp8 && warp >= 6 && !skip) {
-      // ---------------------------------------------------------------- e4m3 to f16
+    } else if (warp >= 6 && !skip) {
+      // ---------------------------------------------------------------- value rows; e4m3 to f16
       const int t = ht - 192;  // 0..63
+      uint32_t edges = 0;      // tiles at the edge so far
+      uint32_t* bad_rows = reinterpret_cast<uint32_t*>(smem + L::kBad);  // [2][4]
+      // Four lanes look over a row each time, for whether it stays; the row's lanes agree.
+      auto row_stays = [&](int j, int row_, bool finite) {
+        const int key = key_a + j * kTile + row_;
+        const bool seen = key >= lo && key < hi;
+        const uint32_t all = __ballot_sync(0xffffffffu, finite);
+        const bool fine = ((all >> (lane & 28)) & 0xFu) == 0xFu;
+        if (seen && !fine && (lane & 3) == 0)
+          atomicOr(bad_rows + 4 * (edges & 1) + (row_ >> 5), 1u << (row_ & 31));
+        return seen && fine;
+      };
+      auto clear_bad = [&] {
+        if (t < 4) bad_rows[4 * (edges & 1) + t] = 0u;
+        named_barrier(3 + half, 64);
+      };
       // one tile of codes (64-byte rows, 64-byte swizzle) to f16 (128-byte rows and swizzle)
-      auto convert = [&](uint32_t src, uint32_t dst) {
+      auto convert = [&](uint32_t src, uint32_t dst, bool look, int j) {
 #pragma unroll 2
         for (int i = t; i < kTile * 4; i += 64) {
           const int r = i >> 2, c = i & 3;
@@ -416,39 +447,91 @@ __global__ void __launch_bounds__(kThreads, 1)
           e4m3x4_to_f16(w.y, x.z, x.w);
           e4m3x4_to_f16(w.z, y.x, y.y);
           e4m3x4_to_f16(w.w, y.z, y.w);
+          if (look) {
+            const bool finite = !(not_finite<true>(x.x) || not_finite<true>(x.y) ||
+                                  not_finite<true>(x.z) || not_finite<true>(x.w) ||
+                                  not_finite<true>(y.x) || not_finite<true>(y.y) ||
+                                  not_finite<true>(y.z) || not_finite<true>(y.w));
+            if (!row_stays(j, r, finite)) x = y = make_uint4(0, 0, 0, 0);
+          }
           sts128(dst + r * 128 + (((2 * c) ^ (r & 7)) << 4), x);
           sts128(dst + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4), y);
         }
         fence_async_smem();
       };
-      // K of tile j+1 before V of tile j: Q K^T runs a tile ahead of P V
-      auto convert_k = [&](int j) {
-        const int s = j % kRaw;
-        if (!ctx.wait_warp(BAR_RAW + s, (j / kRaw) & 1)) return false;
-        if (j > 0 && !ctx.wait_warp(BAR_S_FULL, (j - 1) & 1)) return false;  // the one before is used
-        convert(ctx.sbase + L::kRawK + s * kTile8, ctx.sbase + L::kK);
-        mbar_arrive(ctx.bar(BAR_K_FULL));
-        return true;
-      };
-      bool ok = n_tiles > 0 && convert_k(0);
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        if (j + 1 < n_tiles && !(ok = convert_k(j + 1))) break;
-        if (j > 0 && !(ok = ctx.wait_warp(BAR_PV, (j - 1) & 1))) break;  // V of the one before is used
-        convert(ctx.sbase + L::kRawV + (j % kRaw) * kTile8, ctx.sbase + L::kV);
-        mbar_arrive(ctx.bar(BAR_V_FULL));
-        mbar_arrive(ctx.bar(BAR_RAW_FREE + j % kRaw));
+      if (!kFp8) {
+        for (int j = 0; j < n_tiles; ++j) {
+          // Every tile is waited for and let go, so that the barrier's phase is never lost.
+          if (!ctx.wait_warp(BAR_V_FULL + (j & 1), (j >> 1) & 1)) break;
+          if (!at_edge(j)) {
+            if (lane == 0) mbar_arrive(ctx.bar(BAR_V_FREE + (j & 1)));
+            continue;
+          }
+          clear_bad();
+          const uint32_t vt = ctx.sbase + L::kV + (j & 1) * kTile16;
+          for (int i = t; i < kTile * 4; i += 64) {
+            // a lane's two chunks of its row, others' in other banks
+            const int r = i >> 2;
+            const uint32_t c0 = vt + r * 128 + 16 * ((2 * (i & 3) + r) & 7);
+            const uint32_t c1 = vt + r * 128 + 16 * ((2 * (i & 3) + 1 + r) & 7);
+            const uint4 x = lds128(c0), y = lds128(c1);
+            const bool finite = !(not_finite<false>(x.x) || not_finite<false>(x.y) ||
+                                  not_finite<false>(x.z) || not_finite<false>(x.w) ||
+                                  not_finite<false>(y.x) || not_finite<false>(y.y) ||
+                                  not_finite<false>(y.z) || not_finite<false>(y.w));
+            if (!row_stays(j, r, finite)) {
+              sts128(c0, make_uint4(0, 0, 0, 0));
+              sts128(c1, make_uint4(0, 0, 0, 0));
+            }
+          }
+          fence_async_smem();
+          mbar_arrive(ctx.bar(BAR_SEEN + (edges & 1)));
+          if (lane == 0) mbar_arrive(ctx.bar(BAR_V_FREE + (j & 1)));
+          ++edges;
+        }
+      } else {
+        // K of tile j+1 before V of tile j: Q K^T runs a tile ahead of P V
+        auto convert_k = [&](int j) {
+          const int s = j % kRaw;
+          if (!ctx.wait_warp(BAR_RAW + s, (j / kRaw) & 1)) return false;
+          if (j > 0 && !ctx.wait_warp(BAR_S_FULL, (j - 1) & 1)) return false;  // the one before is used
+          convert(ctx.sbase + L::kRawK + s * kTile8, ctx.sbase + L::kK, false, j);
+          mbar_arrive(ctx.bar(BAR_K_FULL));
+          return true;
+        };
+        bool ok = n_tiles > 0 && convert_k(0);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          if (j + 1 < n_tiles && !(ok = convert_k(j + 1))) break;
+          if (j > 0 && !(ok = ctx.wait_warp(BAR_PV, (j - 1) & 1))) break;  // V of the one before is used
+          const bool look = at_edge(j);
+          if (look) clear_bad();
+          convert(ctx.sbase + L::kRawV + (j % kRaw) * kTile8, ctx.sbase + L::kV, look, j);
+          mbar_arrive(ctx.bar(BAR_V_FULL));
+          if (look) {
+            mbar_arrive(ctx.bar(BAR_SEEN + (edges & 1)));
+            ++edges;
+          }
+          mbar_arrive(ctx.bar(BAR_RAW_FREE + j % kRaw));
+        }
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax
     setmaxnreg_inc<kRegsSoftmax>();
     const int r = ht;  // row = TMEM lane
-    if (warp < active && !skip) {
+    const bool works = warp < active && !skip;
+    float unit = 1.f;
+    if (works)
+      unit = store_query<kFp8>(a, smem, b, t0 + (r >> 3), idx0 + (r >> 3), g * kGroup + (r & 7), r);
+    fence_async_smem();
+    named_barrier(1, kThreads);  // the barriers and the tensor memory are there
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot + half * kHalfCols;
+    if (works) {
       const int t = t0 + (r >> 3);       // token
       const int idx = idx0 + (r >> 3);   // its index
       const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
       const uint32_t tS = tmem + lane_off, tP = tS + kColP, tO = tS + kColO;
-      const float unit = store_query<kFp8>(a, smem, b, t, idx, g * kGroup + (r & 7), r);
       {
         uint32_t z[32];
 #pragma unroll
@@ -457,25 +540,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32(tO + 32, z);
         tmem_st_wait();
       }
-      fence_async_smem();
       tc_fence_before_sync();
       mbar_arrive(ctx.bar(BAR_Q));
 
       float m = kNoMax, l = 0.f;
-      // keys below it, and from it on, are masked for some token of the row
-      const int edge_lo = a.window > 0 ? min(idx0 + kNT, len) - a.window : 0;
-      const int edge_hi = idx0 + 1;
       const int first = a.window > 0 ? idx - a.window + 1 : 0;  // this row sees [first, idx]
       // the other half's barrier for this warp
       const uint32_t other_turn = ctx.bar(BAR_TURN + warp) +
                                   (half ? 0u - L::kHalfBytes : L::kHalfBytes);
       uint32_t edges = 0;  // tiles at the edge so far
-      // all softmax warps meet; a wait like the others, so that none waits for ever
-      auto meet = [&](int step) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ctx.bar(BAR_EDGE + step));
-        return ctx.wait_warp(BAR_EDGE + step, edges & 1);
-      };
       bool ok = true;
       for (int j = 0; j < n_tiles; ++j) {
         if (!(ok = ctx.wait_warp(BAR_S_FULL, j & 1))) break;
@@ -483,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sv[128];
         tmem_ld128_split(tS, sv);
         const int key0 = key_a + j * kTile;
-        const bool edge = key0 + kTile > edge_hi || key0 < edge_lo;
+        const bool edge = at_edge(j);
         const float4* pf = reinterpret_cast<const float4*>(smem + L::kPage + (j % kPageRing) * 128);
         if (!edge) {
           // S is in registers: the next product may overwrite it
@@ -590,36 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         if (edge) {
-          // Value rows that no token sees, or with an infinity or NaN, leave the tile.
-          if (!(ok = ctx.wait_warp(BAR_V_FULL + (kFp8 ? 0 : j & 1), (kFp8 ? j : j >> 1) & 1))) break;
-          uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::kBad) + 4 * (j & 1);
-          uint8_t* vt = smem + L::kV + (kFp8 ? 0 : j & 1) * kTile16;
-          if (r < 4) bad[r] = 0u;
-          if (!(ok = meet(0))) break;
-          for (int k = r; k < kTile; k += 32 * active) {
-            const int key = key0 + k;
-            const bool seen = key >= lo && key < hi;
-            bool out = !seen;
-            if (seen) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                // a chunk of its own per lane: rows lie a whole bank line apart
-                const uint4 w =
-                    *reinterpret_cast<const uint4*>(vt + k * 128 + 16 * ((c + k) & 7));
-                out = out || not_finite<kFp8>(w.x) || not_finite<kFp8>(w.y) ||
-                      not_finite<kFp8>(w.z) || not_finite<kFp8>(w.w);
-              }
-              if (out) atomicOr(bad + (k >> 5), 1u << (k & 31));
-            }
-            if (out) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(vt + k * 128 + 16 * ((c + k) & 7)) =
-                    make_uint4(0, 0, 0, 0);
-            }
-          }
-          fence_async_smem();
-          if (!(ok = meet(1))) break;
+          // value rows that were taken out of the tile
+          if (!(ok = ctx.wait_warp(BAR_SEEN + (edges & 1), (edges >> 1) & 1))) break;
+          const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L::kBad) + 4 * (edges & 1);
           ++edges;
           for (int word = 0; word < 4; ++word) {
             for (uint32_t bits = bad[word]; bits; bits &= bits - 1) {
@@ -715,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (half == 0 && warp == 5) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(*tmem_slot, kTmemCols);
   }
 }
 
