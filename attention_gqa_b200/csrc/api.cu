@@ -681,7 +681,7 @@ static int paged_attention_impl(const gptoss_attn_paged_cache* cache, const void
   a.n = n;
   a.max_pages = max_pages;
   a.groups = a.rows / batch;
-  a.target = paged_target(n, a.rows);
+  paged_plan(&a);
   return launch_paged_attention(maps, a, stream) == cudaSuccess ? GPTOSS_ATTN_OK
                                                                 : GPTOSS_ATTN_ERR_LAUNCH;
 }

@@ -194,6 +194,7 @@ struct PagedAttentionArgs {
   int groups;              // rows (token groups) per sequence
   int rows;                // batch * groups
   int target;              // chunks aimed for
+  bool one_wave;           // no more than that
 };
 
 struct PagedMaps {
@@ -202,7 +203,7 @@ struct PagedMaps {
 
 // Query tokens a row holds, chunks aimed for, and the workspace they need.
 int paged_row_tokens(int n);
-int paged_target(int n, int64_t rows);
+void paged_plan(PagedAttentionArgs* args);
 // Most tiles that a row can have, whatever the lengths. Rows of few tiles are not cut,
 // and then there is no workspace and no second kernel.
 int paged_most_tiles(int row_tokens, int tile, int max_len, int window);

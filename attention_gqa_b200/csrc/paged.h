@@ -47,6 +47,11 @@ GQA_HD int paged_chunk_tiles(int64_t total, int target) {
   return c < kPagedLeast ? kPagedLeast : static_cast<int>(c);
 }
 
+// A longer chunk to try when chunks of `chunk` tiles came to `count`, more than `wave`.
+GQA_HD int paged_longer_chunk(int chunk, int count, int wave) {
+  return static_cast<int>((static_cast<int64_t>(chunk) * count + wave - 1) / wave);
+}
+
 // Chunks of one row (a row without keys has one too: it writes the zeros).
 GQA_HD int paged_row_chunks(int tiles, int chunk) {
   return tiles > chunk && tiles > kPagedWhole ? (tiles + chunk - 1) / chunk : 1;

@@ -118,6 +118,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : 4)
     }
     fence_barrier_init();
   }
+  if (threadIdx.x == 32 * kWarps) {
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+  }
   // The tokens, lengths and pages, and the workspace, may still be in use by
   // the kernel before.
   griddep_wait();
@@ -145,10 +149,6 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : 4)
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
     if (!skip && n_tiles > 0) {
-      if (lane == 0) {
-        prefetch_tensormap(&maps.k);
-        prefetch_tensormap(&maps.v);
-      }
       const int P = 1 << page_log2;
       const int box = P < kPagedTile ? P : kPagedTile;  // keys per copy
       const int boxes = kTile / box;                    // at most 8
@@ -177,6 +177,14 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : 4)
         const int page = __shfl_sync(0xffffffffu, cur.page, ((key >> page_log2) - pbase) & 31);
         const bool load = sub < boxes && key < hi && key + box > lo;
         const int n_load = __popc(__ballot_sync(0xffffffffu, load) & 0xFFu);
+        if (lane == 0)
+          mbar_expect_tx(full_bar(s), 2u * static_cast<uint32_t>(n_load * box) * kRowBytes);
+        __syncwarp();
+        if (load && lane < 16) {
+          const uint32_t dst = sbase + (lane < 8 ? L::kK : L::kV) + s * kTileBytes +
+                               static_cast<uint32_t>(sub * box) * kRowBytes;
+          tma_load_4d(dst, lane < 8 ? &maps.k : &maps.v, full_bar(s), 0, g, key & (P - 1), page);
+        }
         if (kFp8) {
           const int pw = (key0 + sub * 16) >> page_log2;  // page of a block of 16 keys
           const float ks = __shfl_sync(0xffffffffu, cur.ks, (pw - pbase) & 31);
@@ -186,15 +194,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : 4)
                 page_factors(ks, vs);
           __syncwarp();
         }
-        if (lane == 0)
-          mbar_arrive_expect_tx(full_bar(s),
-                                2u * static_cast<uint32_t>(n_load * box) * kRowBytes);
-        __syncwarp();
-        if (load && lane < 16) {
-          const uint32_t dst = sbase + (lane < 8 ? L::kK : L::kV) + s * kTileBytes +
-                               static_cast<uint32_t>(sub * box) * kRowBytes;
-          tma_load_4d(dst, lane < 8 ? &maps.k : &maps.v, full_bar(s), 0, g, key & (P - 1), page);
-        }
+        if (lane == 0) mbar_arrive(full_bar(s));  // and the scales are there
         if (++s == kStages) {
           s = 0;
           phase ^= 1;

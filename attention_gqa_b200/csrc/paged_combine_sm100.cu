@@ -7,16 +7,16 @@ namespace gqa {
 namespace {
 
 // Joins the chunks of the rows that have several, with the sink, normalises and
-// rounds. A CTA of eight warps takes kHeads heads of one token: with one head, every
-// warp takes each eighth chunk and the warps join at the end (few rows, which may
-// have hundreds of chunks); with eight, a warp takes a head (many rows).
+// rounds. A CTA takes kHeads heads of one token. With one head, each of 16 warps
+// takes every sixteenth chunk and the warps join at the end (few rows, which may
+// have many chunks); with eight, a warp takes a head (many rows).
 template <int NT, int kHeads>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttentionArgs a) {
+__global__ void __launch_bounds__(kHeads == 1 ? 512 : 256) paged_combine_kernel(const PagedAttentionArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kSplit = 8 / kHeads;  // warps per head
-  __shared__ float2 part[8][32];
-  __shared__ float2 part_ml[8];
+  constexpr int kSplit = kHeads == 1 ? 16 : 1;  // warps per head
+  __shared__ float2 part[kSplit][32];
+  __shared__ float2 part_ml[kSplit];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int row = static_cast<int>(blockIdx.x);
   const int r = static_cast<int>(blockIdx.y) * kHeads + warp / kSplit;  // token of the row, head
@@ -89,6 +89,7 @@ template <int NT>
 cudaError_t launch(cudaLaunchConfig_t& cfg, const PagedAttentionArgs& a) {
   // the first form while its CTAs, one per output row, are few
   const bool few = static_cast<int64_t>(a.rows) * NT <= 16;
+  cfg.blockDim = dim3(few ? 512 : 256);
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows), NT * (few ? kNumHeads : kNumKvHeads));
   return few ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT, 1>, a)
              : cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT, 8>, a);
@@ -104,7 +105,6 @@ cudaError_t launch_paged_combine(const PagedAttentionArgs& a, int row_tokens, cu
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.blockDim = dim3(256);
   switch (row_tokens) {
     case 1: return launch<1>(cfg, a);
     case 2: return launch<2>(cfg, a);
@@ -114,13 +114,24 @@ cudaError_t launch_paged_combine(const PagedAttentionArgs& a, int row_tokens, cu
 
 int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
 
-// Eight CTAs, one per kv head, make a chunk. Few tokens: about four waves of three CTAs
-// per SM. Many: one wave of two; a row's last chunk is half empty on average, so that
-// many rows' chunks are made longer.
-int paged_target(int n, int64_t rows) {
-  if (paged_row_tokens(n) <= 2) return 148 * 3 * 4 / kNumKvHeads;
-  const int wave = 148 * 2 / kNumKvHeads;
-  return rows < wave ? wave - static_cast<int>(rows / 2) : wave;
+// Chunks that the GPU holds at a time: eight CTAs of the kernel for few tokens, one per kv
+// head, are a chunk, four of the other.
+static int paged_wave(int row_tokens, bool fp8) {
+  const int per_sm = row_tokens == 1 ? (fp8 ? 4 : 3) : 2;
+  return 148 * per_sm / kNumKvHeads;
+}
+
+// Of many rows: chunks aimed for, at most.
+static int paged_target(int row_tokens, bool fp8) {
+  return row_tokens == 1 ? (fp8 ? 111 : 148) : row_tokens == 2 ? 74 : 37;
+}
+
+void paged_plan(PagedAttentionArgs* a) {
+  const int nt = paged_row_tokens(a->n);
+  const int wave = paged_wave(nt, a->cache.fp8);
+  a->one_wave = 2 * static_cast<int64_t>(a->rows) <= wave;
+  a->target = a->one_wave ? wave : paged_target(nt, a->cache.fp8);
+  if (nt == kPagedManyTokens && !a->one_wave && a->rows < wave) a->target -= a->rows / 2;
 }
 
 int paged_most_tiles(int nt, int tile, int max_len, int window) {
@@ -130,13 +141,14 @@ int paged_most_tiles(int nt, int tile, int max_len, int window) {
 }
 
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]) {
-  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(n, 0))) * kNumKvHeads *
-                       paged_row_tokens(n) * kGroup;
+  const int nt = paged_row_tokens(n);
+  // (a wave is fewer chunks, and so are those of e4m3 pages)
+  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(nt, false))) * kNumKvHeads *
+                       nt * kGroup;
   off[0] = 0;
   off[1] = parts * kHeadDim * sizeof(float);
   off[2] = off[1] + parts * sizeof(float2);
   // (the kernel for few tokens takes longer tiles of e4m3 pages, and cuts them less)
-  const int nt = paged_row_tokens(n);
   const int most = paged_most_tiles(nt, nt <= 2 ? kPagedTile : kPagedTileN, max_len, window);
   if (most <= kPagedWhole) return 0;
   return off[2] + ((static_cast<size_t>(rows) * sizeof(int2) + 15) & ~static_cast<size_t>(15));

@@ -69,12 +69,68 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
 // Finds chunk `cid` of the call, by all kThreads threads of the CTA; false past the
 // last one. `sums`: two words per warp. Chunks are counted in the low half of the
 // scanned words, those of rows with several in the high half.
+//
+// Every CTA begins with this, so it is kept short: up to 96 rows the first warp does it
+// alone with sums of 32 bits (no row has more than 2^25 tiles, and 96 make fewer than
+// 2^16 chunks); more are spread over all threads.
 template <int NT, int kTile, int kThreads>
 __device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid, uint64_t* sums,
                                            ScanSlot* slot) {
   constexpr int kWarps = kThreads / 32;
   const int t = static_cast<int>(threadIdx.x);
   const int warp = t >> 5, lane = t & 31;
+  constexpr int kFew = 3;
+  if (a.rows <= 32 * kFew) {
+    if (warp == 0) {
+      const int per = (a.rows + 31) / 32;
+      const int r0 = lane * per, r1 = min(a.rows, r0 + per);
+      if (lane == 0) slot->row = -1;
+      __syncwarp();
+      int tiles[kFew];
+      uint32_t mine = 0;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        tiles[i] = r0 + i < r1 ? row_tiles<NT, kTile>(a, r0 + i) : 0;
+        mine += static_cast<uint32_t>(tiles[i]);
+      }
+      int chunk = paged_chunk_tiles(__reduce_add_sync(0xffffffffu, mine), a.target);
+      int n[kFew];
+      while (true) {
+        mine = 0;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          n[i] = r0 + i < r1 ? paged_row_chunks(tiles[i], chunk) : 0;
+          mine += static_cast<uint32_t>(n[i]) * (n[i] > 1 ? 0x10001u : 1u);
+        }
+        if (!a.one_wave) break;
+        // (ends: chunks grow until every row is one, and those are half a wave at most)
+        const int count = static_cast<int>(__reduce_add_sync(0xffffffffu, mine & 0xFFFFu));
+        if (count <= a.target) break;
+        chunk = paged_longer_chunk(chunk, count, a.target);
+      }
+      uint32_t at = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += u;
+      }
+      at -= mine;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        const int split = cid - static_cast<int>(at & 0xFFFFu);
+        if (split >= 0 && split < n[i]) {
+          slot->row = r0 + i;
+          slot->split = split;
+          slot->chunks = n[i];
+          slot->part = static_cast<int>(at >> 16);
+          slot->len = min(max(__ldg(a.len + (r0 + i) / a.groups), 0), a.max_len);
+        }
+        at += static_cast<uint32_t>(n[i]) * (n[i] > 1 ? 0x10001u : 1u);
+      }
+    }
+    __syncthreads();
+    return slot->row >= 0;
+  }
   const int per = (a.rows + kThreads - 1) / kThreads;
   const int r0 = min(a.rows, t * per), r1 = min(a.rows, r0 + per);
   if (t == 0) slot->row = -1;
