@@ -91,7 +91,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 }
 
 template <bool kFp8, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
     paged_attention_kernel(const __grid_constant__ PagedMaps maps, const PagedAttentionArgs a) {
   using L = Smem<kFp8, NT>;
   constexpr int kStages = Shape<kFp8>::kStages;

@@ -117,19 +117,26 @@ int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
 // Chunks that the GPU holds at a time: eight CTAs of the kernel for few tokens, one per kv
 // head, are a chunk, four of the other.
 static int paged_wave(int row_tokens, bool fp8) {
-  const int per_sm = row_tokens == 1 ? (fp8 ? 4 : 3) : 2;
+  const int per_sm = row_tokens == 1 ? (fp8 ? 4 : 3) : row_tokens == 2 ? 3 : 2;
   return 148 * per_sm / kNumKvHeads;
 }
 
 // Of many rows: chunks aimed for, at most.
 static int paged_target(int row_tokens, bool fp8) {
-  return row_tokens == 1 ? (fp8 ? 111 : 148) : row_tokens == 2 ? 74 : 37;
+  return row_tokens == 1 ? (fp8 ? 111 : 148) : row_tokens == 2 ? 111 : 37;
 }
 
+// A chunk costs about 6 us before its first tile, as much as many tiles, so rows that leave
+// room for it are cut to exactly one wave (1 x 131072 e4m3: 32.7 us against 42.7 with 222
+// chunks; 8 x 32768 e4m3: 57 against 64; 32 ragged rows of 4096 bf16: 32.9 against 38).
+// More rows make uneven chunks, which are better dealt out in one and a half to three
+// waves (64 ragged rows of 8192 e4m3: 62.5 us at 111 chunks, 67.8 at 74, 68.7 at 222; 64
+// full rows bf16: 172 us at 148, 177 at 74). Many tokens: a wave, and less by half a chunk
+// a row, of which the last is half empty on average.
 void paged_plan(PagedAttentionArgs* a) {
   const int nt = paged_row_tokens(a->n);
   const int wave = paged_wave(nt, a->cache.fp8);
-  a->one_wave = 2 * static_cast<int64_t>(a->rows) <= wave;
+  a->one_wave = 4 * static_cast<int64_t>(a->rows) <= 3 * wave;
   a->target = a->one_wave ? wave : paged_target(nt, a->cache.fp8);
   if (nt == kPagedManyTokens && !a->one_wave && a->rows < wave) a->target -= a->rows / 2;
 }

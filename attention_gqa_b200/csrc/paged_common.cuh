@@ -103,7 +103,7 @@ __device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid,
           mine += static_cast<uint32_t>(n[i]) * (n[i] > 1 ? 0x10001u : 1u);
         }
         if (!a.one_wave) break;
-        // (ends: chunks grow until every row is one, and those are half a wave at most)
+        // (ends: chunks grow until every row is one, and the rows are fewer than a wave)
         const int count = static_cast<int>(__reduce_add_sync(0xffffffffu, mine & 0xFFFFu));
         if (count <= a.target) break;
         chunk = paged_longer_chunk(chunk, count, a.target);
