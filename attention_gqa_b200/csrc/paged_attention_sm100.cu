@@ -34,6 +34,10 @@ namespace {
 
 constexpr int kWarps = 4;  // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
+// Three stages leave shared memory for four CTAs of an SM (bf16, with four stages and three
+// CTAs: 64 sequences of a window of 128 12.2 us against 8.1, as they are no longer one wave;
+// the others alike).
+constexpr int kStages = 3;
 // Sixteen-key blocks a warp takes of a tile: two for e4m3, whose work per byte is
 // twice as much, so that the waits and indices of a tile serve 32 keys.
 template <bool kFp8>
@@ -41,15 +45,14 @@ struct Shape {
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kBlocks = kFp8 ? 2 : 1;
   static constexpr int kTile = 16 * kWarps * kBlocks;  // keys
-  static constexpr int kStages = kFp8 ? 3 : 4;
   static constexpr uint32_t kTileBytes = kTile * kHeadDim * kElem;  // one of K or V
 };
 
 template <bool kFp8, int NT>
 struct Smem {
   static constexpr uint32_t kK = 0;
-  static constexpr uint32_t kV = kK + Shape<kFp8>::kStages * Shape<kFp8>::kTileBytes;
-  static constexpr uint32_t kTiles = kV + Shape<kFp8>::kStages * Shape<kFp8>::kTileBytes;
+  static constexpr uint32_t kV = kK + kStages * Shape<kFp8>::kTileBytes;
+  static constexpr uint32_t kTiles = kV + kStages * Shape<kFp8>::kTileBytes;
   // the warps' sums are joined where the tiles were
   static constexpr uint32_t kMergeWarp = NT * kGroup * (kHeadDim + 2) * 4;
   static constexpr uint32_t kMerge = 0;
@@ -59,8 +62,8 @@ struct Smem {
   // float4 [stages][blocks of a tile], e4m3
   static constexpr int kPages = kFp8 ? kWarps * Shape<kFp8>::kBlocks : 0;
   static constexpr uint32_t kPage = kQExp + NT * kGroup * 4;
-  static constexpr uint32_t kBar = kPage + Shape<kFp8>::kStages * kPages * 16;
-  static constexpr uint32_t kScan = kBar + 2 * Shape<kFp8>::kStages * 8;  // 5 + 5 warp sums, slot
+  static constexpr uint32_t kBar = kPage + kStages * kPages * 16;
+  static constexpr uint32_t kScan = kBar + 2 * kStages * 8;  // 5 + 5 warp sums, slot
   static constexpr uint32_t kMisc = kScan + 2 * 5 * 8 + sizeof(ScanSlot);
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
 };
@@ -94,7 +97,6 @@ template <bool kFp8, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
     paged_attention_kernel(const __grid_constant__ PagedMaps maps, const PagedAttentionArgs a) {
   using L = Smem<kFp8, NT>;
-  constexpr int kStages = Shape<kFp8>::kStages;
   constexpr int kTile = Shape<kFp8>::kTile;
   constexpr int kBlocks = Shape<kFp8>::kBlocks;
   constexpr uint32_t kTileBytes = Shape<kFp8>::kTileBytes;

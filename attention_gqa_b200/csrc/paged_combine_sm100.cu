@@ -6,39 +6,66 @@
 namespace gqa {
 namespace {
 
-// Joins the chunks of the rows that have several, with the sink, normalises and
-// rounds. A CTA takes kHeads heads of one token. With one head, each of 16 warps
-// takes every sixteenth chunk and the warps join at the end (few rows, which may
-// have many chunks); with eight, a warp takes a head (many rows).
-template <int NT, int kHeads>
-__global__ void __launch_bounds__(kHeads == 1 ? 512 : 256) paged_combine_kernel(const PagedAttentionArgs a) {
-  griddep_launch_dependents();
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+// Lanes of a head, and heads of a CTA.
+template <int kSplit>
+struct Form {
+  static constexpr int kLanes = kSplit == 1 ? 8 : 32;
+  static constexpr int kHeads = kWarps / kSplit * (32 / kLanes);
+};
+
+// Joins the chunks of the rows that have several, with the sink, normalises and rounds.
+// kSplit > 1 (few rows, of many chunks): so many warps take a head of a token, each every
+// kSplit-th chunk, and join at the end. kSplit = 1: a warp takes four heads. Most rows of a
+// call may have one chunk and nothing to join, so that is what a CTA looks at first.
+// nt: tokens of a row.
+template <int kSplit>
+__global__ void __launch_bounds__(kThreads, 4)
+    paged_combine_kernel(const PagedAttentionArgs a, int nt) {
+  using F = Form<kSplit>;
+  constexpr int kPer = kHeadDim / F::kLanes;  // elements of a lane
   griddep_wait();
-  constexpr int kSplit = kHeads == 1 ? 16 : 1;  // warps per head
-  __shared__ float2 part[kSplit][32];
-  __shared__ float2 part_ml[kSplit];
-  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int row = static_cast<int>(blockIdx.x);
-  const int r = static_cast<int>(blockIdx.y) * kHeads + warp / kSplit;  // token of the row, head
-  const int tk = r / kNumHeads, h = r % kNumHeads;
+  constexpr int kCtas = kNumHeads / F::kHeads;  // of a token
+  const int tk = static_cast<int>(blockIdx.y) / kCtas;
+  const int b = row / a.groups, t = (row - b * a.groups) * nt + tk;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int h = static_cast<int>(blockIdx.y) % kCtas * F::kHeads +
+                (warp / kSplit) * (32 / F::kLanes) + lane / F::kLanes;
+  const int d0 = lane % F::kLanes * kPer;
   const int2 meta = a.meta[row];
-  const int b = row / a.groups, t = (row - b * a.groups) * NT + tk;
-  if (meta.y == 1 || t >= a.n || (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout)) return;
-  const int64_t stride = kNumKvHeads * NT * kGroup;
-  const int64_t first = meta.x * stride + (h / kGroup) * (NT * kGroup) + tk * kGroup + h % kGroup;
-  float M = kNoMax, sum = 0.f, o0 = 0.f, o1 = 0.f;
-  constexpr int kBatch = 8;
+  if (t >= a.n || meta.y == 1 || (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout)) return;
+  // (32 bits: the parts are few, whatever the rows)
+  const int stride = kNumKvHeads * nt * kGroup;
+  const int first = meta.x * stride + (h / kGroup) * (nt * kGroup) + tk * kGroup + h % kGroup;
+  float M = kNoMax, sum = 0.f, o[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+  constexpr int kBatch = kSplit == 1 ? 4 : 8;  // loads in flight
+#pragma unroll 1
   for (int s0 = warp % kSplit; s0 < meta.y; s0 += kBatch * kSplit) {
-    float2 ml[kBatch], v[kBatch];
+    float2 ml[kBatch], v[kBatch][kPer / 2];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int s = s0 + j * kSplit;
       ml[j] = make_float2(kNoMax, 0.f);
-      v[j] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < kPer / 2; ++e) v[j][e] = make_float2(0.f, 0.f);
       if (s < meta.y) {
-        ml[j] = a.part_ml[first + s * stride];
-        v[j] = *reinterpret_cast<const float2*>(a.part_o + (first + s * stride) * kHeadDim +
-                                                2 * lane);
+        const int at = first + s * stride;
+        ml[j] = a.part_ml[at];
+        if constexpr (kPer == 2) {
+          v[j][0] = *reinterpret_cast<const float2*>(a.part_o + at * kHeadDim + d0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPer / 2; e += 2) {
+            const float4 w = *reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + d0 + 2 * e);
+            v[j][e] = make_float2(w.x, w.y);
+            v[j][e + 1] = make_float2(w.z, w.w);
+          }
+        }
       }
     }
     float top = M;
@@ -47,52 +74,68 @@ __global__ void __launch_bounds__(kHeads == 1 ? 512 : 256) paged_combine_kernel(
     const float f = ex2_approx(M - top);
     M = top;
     sum *= f;
-    o0 *= f;
-    o1 *= f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] *= f;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const float fj = ex2_approx(ml[j].x - top);
       sum = fmaf(fj, ml[j].y, sum);
-      o0 = fmaf(fj, v[j].x, o0);
-      o1 = fmaf(fj, v[j].y, o1);
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        o[e] = fmaf(fj, v[j][e / 2].x, o[e]);
+        o[e + 1] = fmaf(fj, v[j][e / 2].y, o[e + 1]);
+      }
     }
   }
+  // Not earlier: a next call's CTAs would take their places while these hold registers, and
+  // no longer fit one wave.
+  griddep_launch_dependents();
   const float sink = __ldg(a.sinks + h) * kLog2e;
   float Mf = fmaxf(sink, M), den;
-  if (kSplit > 1) {
-    part[warp][lane] = make_float2(o0, o1);
+  if constexpr (kSplit > 1) {
+    __shared__ float2 part[kWarps][32];
+    __shared__ float2 part_ml[kWarps];
+    part[warp][lane] = make_float2(o[0], o[1]);
     if (lane == 0) part_ml[warp] = make_float2(M, sum);
     __syncthreads();
-    if (warp > 0) return;
+    if (warp % kSplit != 0) return;
     Mf = sink;
-    for (int w = 0; w < kSplit; ++w) Mf = fmaxf(Mf, part_ml[w].x);
+#pragma unroll 1
+    for (int w = 0; w < kSplit; ++w) Mf = fmaxf(Mf, part_ml[warp + w].x);
     den = ex2_approx(sink - Mf);
-    o0 = o1 = 0.f;
+    o[0] = o[1] = 0.f;
+#pragma unroll 1
     for (int w = 0; w < kSplit; ++w) {
-      const float f = ex2_approx(part_ml[w].x - Mf);
-      den = fmaf(f, part_ml[w].y, den);
-      o0 = fmaf(f, part[w][lane].x, o0);
-      o1 = fmaf(f, part[w][lane].y, o1);
+      const float f = ex2_approx(part_ml[warp + w].x - Mf);
+      den = fmaf(f, part_ml[warp + w].y, den);
+      o[0] = fmaf(f, part[warp + w][lane].x, o[0]);
+      o[1] = fmaf(f, part[warp + w][lane].y, o[1]);
     }
   } else {
     const float f = ex2_approx(M - Mf);
     den = fmaf(f, sum, ex2_approx(sink - Mf));
-    o0 *= f;
-    o1 *= f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] *= f;
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;
-  reinterpret_cast<uint32_t*>(a.out + ((static_cast<int64_t>(b) * a.n + t) * kNumHeads + h) *
-                                          kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
+  uint32_t w[kPer / 2];
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) w[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  uint32_t* out = reinterpret_cast<uint32_t*>(
+      a.out + ((static_cast<int64_t>(b) * a.n + t) * kNumHeads + h) * kHeadDim + d0);
+  if constexpr (kPer == 2) {
+    *out = w[0];
+  } else {
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
-template <int NT>
-cudaError_t launch(cudaLaunchConfig_t& cfg, const PagedAttentionArgs& a) {
-  // the first form while its CTAs, one per output row, are few
-  const bool few = static_cast<int64_t>(a.rows) * NT <= 16;
-  cfg.blockDim = dim3(few ? 512 : 256);
-  cfg.gridDim = dim3(static_cast<unsigned>(a.rows), NT * (few ? kNumHeads : kNumKvHeads));
-  return few ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT, 1>, a)
-             : cudaLaunchKernelEx(&cfg, paged_combine_kernel<NT, 8>, a);
+template <int kSplit>
+cudaError_t launch(cudaLaunchConfig_t& cfg, const PagedAttentionArgs& a, int nt) {
+  using F = Form<kSplit>;
+  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows), nt * kNumHeads / F::kHeads);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<kSplit>, a, nt);
 }
 
 }  // namespace
@@ -105,39 +148,36 @@ cudaError_t launch_paged_combine(const PagedAttentionArgs& a, int row_tokens, cu
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  switch (row_tokens) {
-    case 1: return launch<1>(cfg, a);
-    case 2: return launch<2>(cfg, a);
-    default: return launch<kPagedManyTokens>(cfg, a);
-  }
+  // by the chunks that a row has on average; and eight warps while they are few
+  const int chunks = a.target / a.rows;
+  if (chunks >= 16 && a.rows * row_tokens <= 8) return launch<8>(cfg, a, row_tokens);
+  return chunks >= 8 ? launch<4>(cfg, a, row_tokens) : launch<1>(cfg, a, row_tokens);
 }
 
 int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
 
 // Chunks that the GPU holds at a time: eight CTAs of the kernel for few tokens, one per kv
 // head, are a chunk, four of the other.
-static int paged_wave(int row_tokens, bool fp8) {
-  const int per_sm = row_tokens == 1 ? (fp8 ? 4 : 3) : row_tokens == 2 ? 3 : 2;
+static int paged_wave(int row_tokens) {
+  const int per_sm = row_tokens == 1 ? 4 : row_tokens == 2 ? 3 : 2;
   return 148 * per_sm / kNumKvHeads;
 }
 
 // Of many rows: chunks aimed for, at most.
-static int paged_target(int row_tokens, bool fp8) {
-  return row_tokens == 1 ? (fp8 ? 111 : 148) : row_tokens == 2 ? 111 : 37;
-}
+static int paged_target(int row_tokens) { return row_tokens <= 2 ? 111 : 37; }
 
 // A chunk costs about 6 us before its first tile, as much as many tiles, so rows that leave
-// room for it are cut to exactly one wave (1 x 131072 e4m3: 32.7 us against 42.7 with 222
-// chunks; 8 x 32768 e4m3: 57 against 64; 32 ragged rows of 4096 bf16: 32.9 against 38).
-// More rows make uneven chunks, which are better dealt out in one and a half to three
-// waves (64 ragged rows of 8192 e4m3: 62.5 us at 111 chunks, 67.8 at 74, 68.7 at 222; 64
-// full rows bf16: 172 us at 148, 177 at 74). Many tokens: a wave, and less by half a chunk
-// a row, of which the last is half empty on average.
+// room for it are cut to exactly one wave (1 x 131072 e4m3: 33 us against 43 with 222
+// chunks; 8 x 32768 e4m3: 55 against 64; 32 ragged rows of 4096 bf16: 31 against 36).
+// More rows make uneven chunks, which are better dealt out in more than a wave (64 ragged
+// rows of 8192 e4m3: 61 us at 111 chunks, 67 at 74, 70 at 222; 64 full rows bf16: 167 us
+// at 111, 166 at 74, 174 at 222). Many tokens: a wave, and less by half a chunk a row, of
+// which the last is half empty on average.
 void paged_plan(PagedAttentionArgs* a) {
   const int nt = paged_row_tokens(a->n);
-  const int wave = paged_wave(nt, a->cache.fp8);
+  const int wave = paged_wave(nt);
   a->one_wave = 4 * static_cast<int64_t>(a->rows) <= 3 * wave;
-  a->target = a->one_wave ? wave : paged_target(nt, a->cache.fp8);
+  a->target = a->one_wave ? wave : paged_target(nt);
   if (nt == kPagedManyTokens && !a->one_wave && a->rows < wave) a->target -= a->rows / 2;
 }
 
@@ -149,8 +189,8 @@ int paged_most_tiles(int nt, int tile, int max_len, int window) {
 
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]) {
   const int nt = paged_row_tokens(n);
-  // (a wave is fewer chunks, and so are those of e4m3 pages)
-  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(nt, false))) * kNumKvHeads *
+  // (a wave is no more chunks)
+  const size_t parts = static_cast<size_t>(paged_max_parts(paged_target(nt))) * kNumKvHeads *
                        nt * kGroup;
   off[0] = 0;
   off[1] = parts * kHeadDim * sizeof(float);

@@ -202,6 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Smem<kFp8>;
   constexpr uint32_t kRowBytes = kHeadDim * (kFp8 ? 1 : 2);
   griddep_launch_dependents();
+  if (threadIdx.x == 4 * 32) {
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -291,10 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot + half * kHalfCols;
     if (warp == 4 && !skip) {
       // ---------------------------------------------------------------- producer
-      if (lane == 0) {
-        prefetch_tensormap(&maps.k);
-        prefetch_tensormap(&maps.v);
-      }
       const int P = 1 << page_log2;
       const int box = P < kPagedTile ? P : kPagedTile;  // keys per copy
       const int boxes = kTile / box;                    // 2, 4 or 8
@@ -327,6 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes =
             static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, load) & 0xFFu) * box) * kRowBytes;
         if (kFp8) {
+          if (lane == 0) mbar_expect_tx(ctx.bar(BAR_RAW + s), 2 * bytes);
+          __syncwarp();
+          if (load && lane < 16)
+            tma_load_4d(ctx.sbase + (lane < 8 ? L::kRawK : L::kRawV) + s * kTile8 +
+                            static_cast<uint32_t>(sub * box) * kRowBytes,
+                        lane < 8 ? &maps.k : &maps.v, ctx.bar(BAR_RAW + s), 0, g, key & (P - 1),
+                        page);
           const int pw = (key0 + sub * 16) >> page_log2;  // page of 16 columns
           const float ks = __shfl_sync(0xffffffffu, cur.ks, (pw - pbase) & 31);
           const float vs = __shfl_sync(0xffffffffu, cur.vs, (pw - pbase) & 31);
@@ -334,13 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float4*>(smem + L::kPage + ((i % kPageRing) * 8 + lane) * 16) =
                 page_factors(ks, vs);
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(ctx.bar(BAR_RAW + s), 2 * bytes);
-          __syncwarp();
-          if (load && lane < 16)
-            tma_load_4d(ctx.sbase + (lane < 8 ? L::kRawK : L::kRawV) + s * kTile8 +
-                            static_cast<uint32_t>(sub * box) * kRowBytes,
-                        lane < 8 ? &maps.k : &maps.v, ctx.bar(BAR_RAW + s), 0, g, key & (P - 1),
-                        page);
+          if (lane == 0) mbar_arrive(ctx.bar(BAR_RAW + s));  // and the scales are there
           issued_k = i + 1;
         } else {
           if (lane == 0) mbar_arrive_expect_tx(ctx.bar(BAR_K_FULL + s), bytes);
