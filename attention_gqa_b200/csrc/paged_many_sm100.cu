@@ -50,7 +50,8 @@ constexpr uint32_t kRegsSoftmax = 184;
 static_assert(256 * kRegsLight + 256 * kRegsSoftmax <= 512 * 128, "register split");
 
 // Exp-loop step (of 64 column pairs) at which a softmax warp lets the other half's go on.
-constexpr int kTurnHandOff = 38;
+constexpr int kTurnHandOff = 22;
+constexpr int kAskPv = 56;  // step at which it asks for the products of the tile before
 
 constexpr int kRaw = 3;    // stages of e4m3 tiles
 constexpr int kPageRing = 4;  // tiles whose pages' factors are held: written by the producer up
@@ -67,8 +68,8 @@ struct Smem {
   static constexpr uint32_t kRawV = kRawK + (kFp8 ? kRaw : 0) * kTile8;
   static constexpr uint32_t kPage = kRawV + (kFp8 ? kRaw : 0) * kTile8;  // float4 [ring][8]
   static constexpr uint32_t kBar = kPage + (kFp8 ? kPageRing * 8 * 16 : 0);
-  static constexpr uint32_t kBad = kBar + 32 * 8;  // [2][4] value rows taken out of a tile
-  static constexpr uint32_t kHalfBytes = (kBad + 32 + 1023) / 1024 * 1024;
+  static constexpr uint32_t kBad = kBar + 32 * 8;  // [2][2][4] value rows taken out of a tile
+  static constexpr uint32_t kHalfBytes = (kBad + 64 + 1023) / 1024 * 1024;
   static constexpr uint32_t kScan = 2 * kHalfBytes;  // 16 + 16 warp sums, slot
   static constexpr uint32_t kMisc = kScan + 32 * 8 + sizeof(ScanSlot);  // abort flag, TMEM address
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
@@ -124,6 +125,12 @@ struct Ctx {
   __device__ uint32_t bar(int i) const { return bars + 8u * static_cast<uint32_t>(i); }
   __device__ bool wait(int i, uint32_t parity) const {
     return mbar_wait(bar(i), parity, abort_flag, err, kErrTimeout, kWaitTimeoutNs);
+  }
+  // Whether the phase is over already, asked ahead of the wait so that the answer's latency
+  // passes under other work; for wait_asked.
+  __device__ uint32_t ask(int i, uint32_t parity) const { return mbar_test_wait(bar(i), parity); }
+  __device__ bool wait_asked(uint32_t over, int i, uint32_t parity) const {
+    return __all_sync(0xffffffffu, over) || wait_warp(i, parity);
   }
   __device__ bool wait_warp(int i, uint32_t parity) const {
     return mbar_wait_warp(bar(i), parity, abort_flag, err, kErrTimeout, kWaitTimeoutNs);
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- value rows; e4m3 to f16
       const int t = ht - 192;  // 0..63
       uint32_t edges = 0;      // tiles at the edge so far
-      uint32_t* bad_rows = reinterpret_cast<uint32_t*>(smem + L::kBad);  // [2][4]
+      uint32_t* bad_rows = reinterpret_cast<uint32_t*>(smem + L::kBad) + 4 * (t >> 5);  // this warp's
       // Four lanes look over a row each time, for whether it stays; the row's lanes agree.
       auto row_stays = [&](int j, int row_, bool finite) {
         const int key = key_a + j * kTile + row_;
@@ -430,12 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t all = __ballot_sync(0xffffffffu, finite);
         const bool fine = ((all >> (lane & 28)) & 0xFu) == 0xFu;
         if (seen && !fine && (lane & 3) == 0)
-          atomicOr(bad_rows + 4 * (edges & 1) + (row_ >> 5), 1u << (row_ & 31));
+          atomicOr(bad_rows + 8 * (edges & 1) + (row_ >> 5), 1u << (row_ & 31));
         return seen && fine;
       };
       auto clear_bad = [&] {
-        if (t < 4) bad_rows[4 * (edges & 1) + t] = 0u;
-        named_barrier(3 + half, 64);
+        if (lane < 4) bad_rows[8 * (edges & 1) + lane] = 0u;
+        __syncwarp();
       };
       // one tile of codes (64-byte rows, 64-byte swizzle) to f16 (128-byte rows and swizzle)
       auto convert = [&](uint32_t src, uint32_t dst, bool look, int j) {
@@ -551,13 +558,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   (half ? 0u - L::kHalfBytes : L::kHalfBytes);
       uint32_t edges = 0;  // tiles at the edge so far
       bool ok = true;
+      uint32_t s_over = 0;
       for (int j = 0; j < n_tiles; ++j) {
-        if (!(ok = ctx.wait_warp(BAR_S_FULL, j & 1))) break;
+        if (!(ok = ctx.wait_asked(s_over, BAR_S_FULL, j & 1))) break;
         tc_fence_after_sync();
         uint32_t sv[128];
         tmem_ld128_split(tS, sv);
         const int key0 = key_a + j * kTile;
         const bool edge = at_edge(j);
+        const uint32_t turn_over = ctx.ask(BAR_TURN + warp, (half ? j : j - 1) & 1);
         const float4* pf = reinterpret_cast<const float4*>(smem + L::kPage + (j % kPageRing) * 128);
         if (!edge) {
           // S is in registers: the next product may overwrite it
@@ -606,12 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // The halves' warps of a scheduler take turns: half 0 tile j, half 1 tile j, half 0
         // tile j+1, ...
-        if ((j > 0 || half == 1) && !(ok = ctx.wait_warp(BAR_TURN + warp, (half ? j : j - 1) & 1)))
+        if ((j > 0 || half == 1) &&
+            !(ok = ctx.wait_asked(turn_over, BAR_TURN + warp, (half ? j : j - 1) & 1)))
           break;
         // P and the sums' terms; a thread's 128 exponentials, packed in place
         const uint64_t c2 = f2_pack(kScaleLog2, kScaleLog2);
         const uint64_t nm2 = f2_pack(-m, -m);
         uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+        uint32_t pv_over = 0;
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
           float x0, x1, x2, x3;
@@ -625,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc1 = fadd2(acc1, f2_pack(p2, p3));
           sv[i] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           sv[i + 1] = kFp8 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
+          if (i == kAskPv) pv_over = ctx.ask(BAR_PV, (j - 1) & 1);
           if (i == kTurnHandOff) {
             __syncwarp();
             if (lane == 0) mbar_arrive(other_turn);
@@ -644,8 +656,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += (s0 + s1) + (s2 + s3);
         }
         // P and O are this warpgroup's once the previous tile's P V is done
-        if (j > 0 && !(ok = ctx.wait_warp(BAR_PV, (j - 1) & 1))) break;
+        if (j > 0 && !(ok = ctx.wait_asked(pv_over, BAR_PV, (j - 1) & 1))) break;
         tc_fence_after_sync();
+        s_over = ctx.ask(BAR_S_FULL, (j + 1) & 1);
         {
           uint32_t pw[64];
 #pragma unroll
@@ -666,10 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) {
           // value rows that were taken out of the tile
           if (!(ok = ctx.wait_warp(BAR_SEEN + (edges & 1), (edges >> 1) & 1))) break;
-          const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L::kBad) + 4 * (edges & 1);
+          const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L::kBad) + 8 * (edges & 1);
           ++edges;
           for (int word = 0; word < 4; ++word) {
-            for (uint32_t bits = bad[word]; bits; bits &= bits - 1) {
+            for (uint32_t bits = bad[word] | bad[4 + word]; bits; bits &= bits - 1) {
               const int k = 32 * word + __ffs(bits) - 1;
               const int key = key0 + k;
               float s = tmem_ld1(tS + k);
