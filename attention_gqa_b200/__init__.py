@@ -562,6 +562,18 @@ def _max_pages(table: torch.Tensor) -> int:
     return table.shape[1]
 
 
+def _empty_on(stream, like: torch.Tensor, shape) -> torch.Tensor:
+    """Memory of the type and device of `like` that `stream` may write at once; what the
+    current stream still does to memory that it has given back is not waited for, so
+    with another stream it is taken from that one's own."""
+    if stream is None:
+        return like.new_empty(shape)
+    with torch.cuda.stream(stream):
+        made = like.new_empty(shape)
+    made.record_stream(torch.cuda.current_stream(like.device))  # where its user may use it
+    return made
+
+
 def _call_on(index: int, stream, fn, *args) -> int:
     """fn(*args, stream) with device `index` current, on `stream` or its current one."""
     handle = stream.cuda_stream if stream is not None else \
@@ -633,10 +645,8 @@ def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, p
     window = int(window)
     lib = _load()
     fn = lib.gptoss_attn_paged_attention_yarn if _rope(rope) else lib.gptoss_attn_paged_attention
-    made = []
     if out is None:
-        out = q.new_empty(shape)
-        made.append(out)
+        out = _empty_on(stream, q, shape)
         out_at = out.data_ptr()
     else:
         out_at = _array(out, _BF16, shape, "out", index)
@@ -644,13 +654,9 @@ def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, p
         need = lib.gptoss_attn_paged_attention_workspace_bytes(
             B, n, max_pages * cache.page_size, window)
         if need:
-            workspace = q.new_empty(need // 2)
-            made.append(workspace)
+            workspace = _empty_on(stream, q, need // 2)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of the call")
-    if stream is not None:
-        for t in made:  # the current stream's, but `stream` uses them
-            t.record_stream(stream)
     ws_at, ws_bytes = (None, 0) if workspace is None else \
         (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = _call_on(index, stream, fn, cache, q.data_ptr(), qb, qt, pos_at, table_at, sinks_at,

@@ -193,20 +193,20 @@ struct PagedAttentionArgs {
   int batch, n, max_pages, max_len, window;
   int groups;              // rows (token groups) per sequence
   int rows;                // batch * groups
+  int most;                // tiles of a row at most
   int target;              // chunks aimed for
   bool one_wave;           // no more than that
+  bool none_cut;           // every row is one chunk
 };
 
 struct PagedMaps {
   CUtensorMap k, v;        // boxes (64, 1, min(page, 64), 1)
 };
 
-// Query tokens a row holds, chunks aimed for, and the workspace they need.
+// Query tokens a row holds, how rows are cut (sets most to none_cut), and the workspace
+// for it: none where no row can be cut.
 int paged_row_tokens(int n);
 void paged_plan(PagedAttentionArgs* args);
-// Most tiles that a row can have, whatever the lengths. Rows of few tiles are not cut,
-// and then there is no workspace and no second kernel.
-int paged_most_tiles(int row_tokens, int tile, int max_len, int window);
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]);
 cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& args,
                                    cudaStream_t stream);

@@ -36,6 +36,15 @@ GQA_HD int paged_row_tiles(int lo, int hi, int tile) {
 // Rows of at most this many tiles are one chunk: a chunk's own latency is that
 // of many tiles, and a row that is not cut needs no second kernel.
 constexpr int kPagedWhole = 8;
+// Calls of so many rows cut none: their CTAs fill the GPU many times over, and each would
+// have to look at all the lengths to find its chunk.
+constexpr int kPagedManyRows = 1024;
+
+// Whether no row is cut, of rows with at most `most` tiles.
+GQA_HD bool paged_none_cut(int64_t rows, int most) {
+  return most <= kPagedWhole || rows >= kPagedManyRows;
+}
+
 // No chunk of a longer row has fewer tiles than this, unless the division of its
 // tiles into equal parts leaves one less.
 constexpr int kPagedLeast = 4;
@@ -60,7 +69,7 @@ GQA_HD int paged_row_chunks(int tiles, int chunk) {
 // Chunks of a whole call are at most this many, when no row has more than `most`
 // tiles: sum of max(1, ceil(tiles/c)), with c >= total/target and c >= kPagedLeast.
 GQA_HD int64_t paged_max_chunks(int64_t rows, int most, int target) {
-  if (most <= kPagedWhole) return rows;
+  if (paged_none_cut(rows, most)) return rows;
   const int64_t cut = rows * most / kPagedLeast;
   return rows + (cut < target ? cut : target);
 }

@@ -592,13 +592,12 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttentionArgs& a, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  const int most = paged_most_tiles(NT, Shape<kFp8>::kTile, a.max_len, a.window);
-  const int64_t chunks = paged_max_chunks(a.rows, most, a.target);
+  const int64_t chunks = paged_max_chunks(a.rows, a.most, a.target);
   cfg.gridDim = dim3(static_cast<unsigned>(chunks * kNumKvHeads));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   e = cudaLaunchKernelEx(&cfg, paged_attention_kernel<kFp8, NT>, maps, a);
-  if (e != cudaSuccess || most <= kPagedWhole) return e;
+  if (e != cudaSuccess || a.none_cut) return e;
   return launch_paged_combine(a, NT, stream);
 }
 

@@ -166,6 +166,12 @@ static int paged_wave(int row_tokens) {
 // Of many rows: chunks aimed for, at most.
 static int paged_target(int row_tokens) { return row_tokens <= 2 ? 111 : 37; }
 
+static int paged_most_tiles(int nt, int tile, int max_len, int window) {
+  // a row of nt tokens sees window + nt - 1 keys, from anywhere in a tile
+  return paged_row_tiles(0, window > 0 && window + nt + tile < max_len ? window + nt + tile : max_len,
+                         tile);
+}
+
 // A chunk costs about 6 us before its first tile, as much as many tiles, so rows that leave
 // room for it are cut to exactly one wave (1 x 131072 e4m3: 33 us against 43 with 222
 // chunks; 8 x 32768 e4m3: 55 against 64; 32 ragged rows of 4096 bf16: 31 against 36).
@@ -176,15 +182,12 @@ static int paged_target(int row_tokens) { return row_tokens <= 2 ? 111 : 37; }
 void paged_plan(PagedAttentionArgs* a) {
   const int nt = paged_row_tokens(a->n);
   const int wave = paged_wave(nt);
+  a->most = paged_most_tiles(nt, nt <= 2 && !a->cache.fp8 ? kPagedTile : kPagedTileN, a->max_len,
+                             a->window);
+  a->none_cut = paged_none_cut(a->rows, a->most);
   a->one_wave = 4 * static_cast<int64_t>(a->rows) <= 3 * wave;
   a->target = a->one_wave ? wave : paged_target(nt);
   if (nt == kPagedManyTokens && !a->one_wave && a->rows < wave) a->target -= a->rows / 2;
-}
-
-int paged_most_tiles(int nt, int tile, int max_len, int window) {
-  // a row of nt tokens sees window + nt - 1 keys, from anywhere in a tile
-  return paged_row_tiles(0, window > 0 && window + nt + tile < max_len ? window + nt + tile : max_len,
-                         tile);
 }
 
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]) {

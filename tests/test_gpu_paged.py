@@ -140,7 +140,8 @@ def _attend(q, k, v, sinks, index, window):
     return out, size, vmax
 
 
-def _check_attention(got, cache, q, sinks, lengths, window, rope="plain", pos=None, what=""):
+def _check_attention(got, cache, q, sinks, lengths, window, rope="plain", pos=None, what="",
+                     only=None):
     B, n = q.shape[0], q.shape[1]
     got = dev_to_f64(got).reshape(B, n, 64, 64)
     qf, sk = _f64(q.float()), _f64(sinks)
@@ -149,6 +150,8 @@ def _check_attention(got, cache, q, sinks, lengths, window, rope="plain", pos=No
     assert np.all(np.isfinite(got)), what
     off = norm = 0.0
     for b, length in enumerate(lengths):
+        if only is not None and b not in only:
+            continue
         k, v = cache.sequence(b, length)
         for t in range(n):
             i = length - n + t
@@ -451,6 +454,45 @@ def test_attention_split(cuda_device, dtype, n, lengths):
                               pos=pos.cuda(), **cache.scales())
     gqa.check()
     _check_attention(out, cache, q, sinks, lengths, 0, pos=pos)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n", [(96, 1), (97, 1), (250, 2), (40, 70), (1030, 1), (520, 17)])
+def test_attention_of_many_rows(cuda_device, dtype, B, n):
+    """Around the counts of rows at which the work is planned in another way, with a few long
+    sequences among short ones; those, and some others, are looked at."""
+    rng = np.random.default_rng(B + n)
+    lengths = [int(x) for x in rng.integers(0, 30, B)]
+    long = [0, B // 2, B - 1]
+    for i, b in enumerate(long):
+        lengths[b] = 2500 - 700 * i
+    g = torch.Generator().manual_seed(B)
+    cache = Cache(lengths, 64, dtype, seed=n)
+    cache.fill(lengths, g)
+    q, sinks = _queries(B, n, g)
+    only = set(long) | {int(x) for x in rng.integers(0, B, 8)}
+    for window in (0, 100):
+        out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int(lengths),
+                                  window=window, **cache.scales())
+        gqa.check()
+        _check_attention(out, cache, q, sinks, lengths, window, only=only)
+        assert all(not out[b].any() for b in range(B) if lengths[b] == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 2, 16, 33])
+@pytest.mark.parametrize("batch", [1, 7, 26, 30])
+def test_attention_of_equal_and_unequal_rows_in_a_wave(cuda_device, dtype, n, batch):
+    """Rows cut to one wave of chunks: every row alike, and one much longer than the others."""
+    g = torch.Generator().manual_seed(batch)
+    for lengths in ([1300] * batch, [3900] + [150] * (batch - 1)):
+        cache = Cache(lengths, 128, dtype, seed=n)
+        cache.fill(lengths, g)
+        q, sinks = _queries(batch, n, g)
+        out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int(lengths),
+                                  **cache.scales())
+        gqa.check()
+        _check_attention(out, cache, q, sinks, lengths, 0, only={0, batch - 1})
 
 
 def test_attention_matches_contiguous_decode(cuda_device):
@@ -807,6 +849,30 @@ def test_two_streams_at_once(cuda_device):
         cache, lengths, _, q, sinks = runs[i]
         _check_attention(outs[i][0], cache, q, sinks, lengths, 0)
         assert all(torch.equal(o, outs[i][0]) for o in outs[i][1:])
+
+
+def test_another_stream_takes_no_memory_that_the_current_one_still_writes(cuda_device):
+    g = torch.Generator().manual_seed(19)
+    lengths = [2000] * 8
+    cache = Cache(lengths, 64, torch.bfloat16)
+    cache.fill(lengths, g)
+    q, sinks = _queries(8, 1, g)
+    ln, other = _int(lengths), torch.cuda.Stream()
+    want = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, ln)
+    need = gqa.paged_attention_workspace_bytes(8, 1, cache.table.shape[1] * 64)
+    a = torch.zeros(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(40):  # tens of milliseconds of the current stream
+        a = a @ a
+    given_back = [torch.empty(x, dtype=torch.bfloat16, device="cuda")
+                  for x in (q.shape, (need // 2,))]
+    for x in given_back:
+        x.fill_(float("nan"))
+    del x, given_back
+    out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, ln, stream=other)
+    torch.cuda.synchronize()
+    gqa.check(other)
+    assert torch.equal(out, want)
 
 
 def test_paged_attention_skips_work_while_a_timeout_is_pending(cuda_device):
