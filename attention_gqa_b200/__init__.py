@@ -28,6 +28,7 @@ rotation must be read with the same one.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -567,6 +568,8 @@ def _empty_on(stream, like: torch.Tensor, shape) -> torch.Tensor:
     current stream still does to memory that it has given back is not waited for, so
     with another stream it is taken from that one's own."""
     if stream is None:
+        if like.shape == shape and like.is_contiguous():
+            return torch.empty_like(like)  # (the faster call)
         return like.new_empty(shape)
     with torch.cuda.stream(stream):
         made = like.new_empty(shape)
@@ -615,6 +618,7 @@ def paged_append(k, v, pos, kpages, vpages, table, lengths, counts=None, kscales
         _raise(st, "gptoss_attn_paged_append")
 
 
+@functools.lru_cache(maxsize=256)  # a function of the sizes alone
 def paged_attention_workspace_bytes(batch: int, n: int, max_len: int, window: int = 0) -> int:
     """Workspace of paged_attention(); 0 where no row of queries can be cut."""
     return int(_load().gptoss_attn_paged_attention_workspace_bytes(batch, n, max_len, int(window)))
@@ -651,8 +655,7 @@ def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, p
     else:
         out_at = _array(out, _BF16, shape, "out", index)
     if workspace is None:
-        need = lib.gptoss_attn_paged_attention_workspace_bytes(
-            B, n, max_pages * cache.page_size, window)
+        need = paged_attention_workspace_bytes(B, n, max_pages * cache.page_size, window)
         if need:
             workspace = _empty_on(stream, q, need // 2)
     elif workspace.get_device() != index or not workspace.is_contiguous():
