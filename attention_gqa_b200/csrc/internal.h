@@ -194,8 +194,9 @@ struct PagedAttentionArgs {
   int groups;              // rows (token groups) per sequence
   int rows;                // batch * groups
   int most;                // tiles of a row at most
-  int target;              // chunks aimed for
-  bool one_wave;           // no more than that
+  int wave;                // chunks that the GPU holds at a time
+  int target;              // chunks aimed for, if not one wave
+  bool one_wave;           // no more chunks than that
   bool none_cut;           // every row is one chunk
 };
 

@@ -61,6 +61,20 @@ GQA_HD int paged_longer_chunk(int chunk, int count, int wave) {
   return static_cast<int>((static_cast<int64_t>(chunk) * count + wave - 1) / wave);
 }
 
+// Estimated time, in `wave`-ths of a tile's, of `count` chunks of at most `longest` and
+// together `total` tiles on `wave` places, for the kernel for many tokens: a chunk costs
+// three tiles before its first, and joining cut rows two in all. Equal chunks run in whole
+// waves, unequal ones are dealt out as places get free.
+GQA_HD int64_t paged_estimate(int64_t total, int count, int longest, int wave, bool cut) {
+  const int64_t one = longest + 3;
+  int64_t t = (count + wave - 1) / wave * wave * one;
+  if (count > wave) {
+    const int64_t dealt = total + 3 * static_cast<int64_t>(count) + wave * one / 2;
+    t = dealt < t ? dealt : t;
+  }
+  return t + (cut ? 2 * wave : 0);
+}
+
 // Chunks of one row (a row without keys has one too: it writes the zeros).
 GQA_HD int paged_row_chunks(int tiles, int chunk) {
   return tiles > chunk && tiles > kPagedWhole ? (tiles + chunk - 1) / chunk : 1;

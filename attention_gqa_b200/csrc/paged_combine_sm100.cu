@@ -163,8 +163,8 @@ static int paged_wave(int row_tokens) {
   return 148 * per_sm / kNumKvHeads;
 }
 
-// Of many rows: chunks aimed for, at most.
-static int paged_target(int row_tokens) { return row_tokens <= 2 ? 111 : 37; }
+// Chunks aimed for beyond one wave.
+static int paged_target(int row_tokens) { return row_tokens <= 2 ? 111 : 55; }
 
 static int paged_most_tiles(int nt, int tile, int max_len, int window) {
   // a row of nt tokens sees window + nt - 1 keys, from anywhere in a tile
@@ -175,19 +175,21 @@ static int paged_most_tiles(int nt, int tile, int max_len, int window) {
 // A chunk costs about 6 us before its first tile, as much as many tiles, so rows that leave
 // room for it are cut to exactly one wave (1 x 131072 e4m3: 33 us against 43 with 222
 // chunks; 8 x 32768 e4m3: 55 against 64; 32 ragged rows of 4096 bf16: 31 against 36).
-// More rows make uneven chunks, which are better dealt out in more than a wave (64 ragged
+// More rows make uneven chunks, which are better dealt out in a wave and a half (64 ragged
 // rows of 8192 e4m3: 61 us at 111 chunks, 67 at 74, 70 at 222; 64 full rows bf16: 167 us
-// at 111, 166 at 74, 174 at 222). Many tokens: a wave, and less by half a chunk a row, of
-// which the last is half empty on average.
+// at 111, 166 at 74, 174 at 222). With many tokens a chunk has its SM alone and its time
+// is known better, so the device estimates whether whole rows end first (36 full rows of
+// 8192 e4m3, five tokens each: 139 us whole, 152 cut; 36 ragged ones: 124 and 103; eight
+// pieces of 40 on 32768: 555 us whole, 397 cut).
 void paged_plan(PagedAttentionArgs* a) {
   const int nt = paged_row_tokens(a->n);
-  const int wave = paged_wave(nt);
-  a->most = paged_most_tiles(nt, nt <= 2 && !a->cache.fp8 ? kPagedTile : kPagedTileN, a->max_len,
+  const bool many = nt == kPagedManyTokens;
+  a->wave = paged_wave(nt);
+  a->most = paged_most_tiles(nt, !many && !a->cache.fp8 ? kPagedTile : kPagedTileN, a->max_len,
                              a->window);
   a->none_cut = paged_none_cut(a->rows, a->most);
-  a->one_wave = 4 * static_cast<int64_t>(a->rows) <= 3 * wave;
-  a->target = a->one_wave ? wave : paged_target(nt);
-  if (nt == kPagedManyTokens && !a->one_wave && a->rows < wave) a->target -= a->rows / 2;
+  a->one_wave = a->rows <= (many ? a->wave / 2 : 3 * a->wave / 4);
+  a->target = a->one_wave ? a->wave : paged_target(nt);
 }
 
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]) {

@@ -104,20 +104,35 @@ __device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid,
         tiles[i] = r0 + i < r1 ? row_tiles<NT, kTile>(a, r0 + i) : 0;
         mine += static_cast<uint32_t>(tiles[i]);
       }
-      int chunk = paged_chunk_tiles(__reduce_add_sync(0xffffffffu, mine), a.target);
+      const uint32_t total = __reduce_add_sync(0xffffffffu, mine);
       int n[kFew];
-      while (true) {
+      int count;
+      auto cut = [&](int chunk) {  // into chunks of so many tiles
         mine = 0;
 #pragma unroll
         for (int i = 0; i < kFew; ++i) {
           n[i] = r0 + i < r1 ? paged_row_chunks(tiles[i], chunk) : 0;
           mine += static_cast<uint32_t>(n[i]) * (n[i] > 1 ? 0x10001u : 1u);
         }
-        if (!a.one_wave) break;
+        count = static_cast<int>(__reduce_add_sync(0xffffffffu, mine & 0xFFFFu));
+      };
+      int chunk = paged_chunk_tiles(total, a.target);
+      cut(chunk);
+      if (a.one_wave) {
         // (ends: chunks grow until every row is one, and the rows are fewer than a wave)
-        const int count = static_cast<int>(__reduce_add_sync(0xffffffffu, mine & 0xFFFFu));
-        if (count <= a.target) break;
-        chunk = paged_longer_chunk(chunk, count, a.target);
+        while (count > a.wave) cut(chunk = paged_longer_chunk(chunk, count, a.wave));
+      } else if constexpr (NT > 2) {
+        int tail = 0, whole = 0;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          if (n[i] > 0) tail = max(tail, (tiles[i] + n[i] - 1) / n[i]);
+          whole = max(whole, tiles[i]);
+        }
+        tail = __reduce_max_sync(0xffffffffu, tail);
+        whole = __reduce_max_sync(0xffffffffu, whole);
+        if (paged_estimate(total, a.rows, whole, a.wave, false) <=
+            paged_estimate(total, count, tail, a.wave, true))
+          cut(whole);
       }
       uint32_t at = mine;
 #pragma unroll

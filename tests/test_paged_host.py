@@ -28,6 +28,11 @@ int chunk_tiles(long long total, int target) { return paged_chunk_tiles(total, t
 int row_chunks(int tiles, int chunk) { return paged_row_chunks(tiles, chunk); }
 long long max_chunks(long long rows, int most, int target) { return paged_max_chunks(rows, most, target); }
 long long max_parts(int target) { return paged_max_parts(target); }
+int longer_chunk(int chunk, int count, int wave) { return paged_longer_chunk(chunk, count, wave); }
+long long estimate(long long total, int count, int longest, int wave, int cut) {
+  return paged_estimate(total, count, longest, wave, cut);
+}
+int none_cut(long long rows, int most) { return paged_none_cut(rows, most); }
 void chunk_range(int tiles, int chunks, int i, int* out) {
   paged_chunk_range(tiles, chunks, i, out, out + 1);
 }
@@ -46,7 +51,9 @@ def host(tmp_path_factory):
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, str(src), "-o",
                     str(so)], check=True)
     lib = ctypes.CDLL(str(so))
-    lib.max_chunks.restype = lib.max_parts.restype = ctypes.c_longlong
+    lib.max_chunks.restype = lib.max_parts.restype = lib.estimate.restype = ctypes.c_longlong
+    lib.estimate.argtypes = [ctypes.c_longlong] + 4 * [ctypes.c_int]
+    lib.none_cut.argtypes = [ctypes.c_longlong, ctypes.c_int]
     lib.max_chunks.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
     lib.chunk_tiles.argtypes = [ctypes.c_longlong, ctypes.c_int]
     lib.scale_bits.restype = ctypes.c_uint
@@ -114,6 +121,48 @@ def test_chunks_cover_every_tile_once_within_the_grid_and_the_workspace(host, ta
         for most in (max(tiles), max(tiles) + 1, 2048):
             assert chunks <= host.max_chunks(len(tiles), most, target)
         assert parts <= host.max_parts(target)
+
+
+@pytest.mark.parametrize("wave", [37, 55, 74])
+def test_few_rows_are_cut_to_one_wave(host, wave):
+    """Chunks grow until they fit, in a few steps, and are no longer than they have to be but
+    for the rounding of the rows' own divisions."""
+    rng = random.Random(wave)
+    for _ in range(500):
+        rows = rng.randint(1, 3 * wave // 4)
+        tiles = [int(2 ** rng.uniform(0, 11)) for _ in range(rows)]
+        if rng.random() < 0.3:
+            tiles = [tiles[0]] * rows
+        c = first = host.chunk_tiles(sum(tiles), wave)
+        count = sum(host.row_chunks(t, c) for t in tiles)
+        steps = 0
+        while count > wave:
+            longer = host.longer_chunk(c, count, wave)
+            assert longer > c
+            c, steps = longer, steps + 1
+            count = sum(host.row_chunks(t, c) for t in tiles)
+        assert steps < 40 and c <= max(first, 2 * max(tiles))
+        assert count <= host.max_chunks(rows, max(tiles), wave)
+        assert sum(n for t in tiles if (n := host.row_chunks(t, c)) > 1) <= wave
+
+
+def test_estimates_order_the_cuts_as_they_were_measured(host):
+    def time(tiles, chunk):
+        n = [host.row_chunks(t, chunk) for t in tiles]
+        longest = max(-(-t // k) for t, k in zip(tiles, n))
+        return host.estimate(sum(tiles), sum(n), longest, 37, max(n) > 1)
+    whole = 2 ** 31 - 1
+    for tiles in ([64] * 36, [36] * 32, [64] * 64):
+        assert time(tiles, whole) <= time(tiles, host.chunk_tiles(sum(tiles), 55))  # ties: whole
+    ragged = [64 * i // 36 for i in range(1, 37)]
+    for tiles in (ragged, [256] * 24, [32] * 3 + [5] * 40):
+        assert time(tiles, whole) > time(tiles, host.chunk_tiles(sum(tiles), 55))
+
+
+def test_none_is_cut_of_short_or_very_many_rows(host):
+    assert host.none_cut(1, 8) and not host.none_cut(1, 9)
+    assert not host.none_cut(1023, 9) and host.none_cut(1024, 2048)
+    assert host.max_chunks(1024, 2048, 111) == 1024
 
 
 def test_scale_is_the_least_power_of_two_that_holds_the_value(host):
