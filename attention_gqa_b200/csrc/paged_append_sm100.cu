@@ -9,8 +9,11 @@
 //   s = max(s of the page's earlier tokens, least 2^e with max |x| <= 448 * 2^e).
 // Infinities saturate and NaN stays; neither decides the scale.
 //
-// Both kernels are bound by HBM: 256 bytes read per token and kv head, 256 (bf16)
-// or 128 (e4m3) written.
+// Both kernels have HBM's floor: 256 bytes read per token and kv head, 256 (bf16) or 128
+// (e4m3) written. Measured on a B200 for 4 x 16384 tokens: bf16 43.3 us, 6.2 TB/s of that;
+// e4m3 57.4 us, 3.5 TB/s, its CTAs waiting in turn for their tokens and for their largest
+// value (the issue slots are 56 % used, and 64 registers a thread allow two CTAs of 512
+// per SM). One token of 64 sequences: 1.7 and 2.6 us on the device, less than a launch.
 #include "internal.h"
 #include "paged.h"
 #include "sm100_ptx.cuh"
@@ -190,7 +193,9 @@ constexpr int kAppendWarps = 16;  // most warps of a CTA
 // a head as above (1 KB per load, and one table row for all heads); kTokens is how
 // many that can be. Tokens are read once and kept (the first four; a warp has more only
 // in pages of 128), for the largest value of each head, over the CTA, and then for
-// the codes.
+// the codes. Tried for those 4 x 16384 tokens (57.4 us): a warp per (page, head) that reads
+// twice, 90 us; one CTA for a page's keys and values, 63 to 70; 256 threads with half of
+// the tokens read again, 60.6; 40 registers and three CTAs, 69.
 template <int kTokens>
 __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     append_e4m3_kernel(const PagedAppendArgs a) {

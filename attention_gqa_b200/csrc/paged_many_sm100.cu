@@ -28,8 +28,13 @@
 // or NaN, are zeroed in shared memory; the latter are noted, and the softmax warps add
 // them to the queries that see them one by one (exact, and as slow as it is rare).
 //
-// Bound by the exponential unit for whole rows: 128 x 128 of them per tile take 1024
-// cycles of an SM.
+// The floor of whole rows is the exponential unit: 128 x 128 of them per tile take 1024
+// cycles of an SM. A pair of halves takes about 3000 for its two tiles, as a row's thread has
+// its loads, maximum, exponentials and stores one after the other and only the other
+// half's beside them: 512 tokens on 4096 cached ones take 78 us (bf16; 470 TFLOP/s) and 89
+// (e4m3), of which 32 chunks of 33 to 36 tiles on 37 places. Before the first tile a CTA
+// spends about 5.5 us. Two threads per row, of 64 columns each, which tell each other
+// their maximum, took 96 to 114 us.
 #include "paged_common.cuh"
 
 namespace gqa {
@@ -49,7 +54,8 @@ constexpr uint32_t kRegsLight = 72;
 constexpr uint32_t kRegsSoftmax = 184;
 static_assert(256 * kRegsLight + 256 * kRegsSoftmax <= 512 * 128, "register split");
 
-// Exp-loop step (of 64 column pairs) at which a softmax warp lets the other half's go on.
+// Exp-loop step (of 64 column pairs) at which a softmax warp lets the other half's go on
+// (22: 77.9 us, 30: 78.8, 38: 79.1 for 512 bf16 tokens on 4096; 2 to 18 were no better).
 constexpr int kTurnHandOff = 22;
 constexpr int kAskPv = 56;  // step at which it asks for the products of the tile before
 
