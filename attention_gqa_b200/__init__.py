@@ -530,15 +530,19 @@ def _paged_cache(kpages, vpages, kscales, vscales, index: int) -> _PagedCache:
     if dtype is not _BF16 and dtype is not _E4M3:
         raise TypeError("kpages must be bfloat16 or float8_e4m3fn, got %s" % dtype)
     shape, stride = kpages.shape, kpages.stride()
-    if len(shape) != 4 or shape[1] not in PAGE_SIZES or shape[2] != NUM_KV_HEADS or \
-            shape[3] != HEAD_DIM:
+    if len(shape) == 4:
+        num, page, heads, dim = shape
+    else:
+        num = page = heads = dim = 0
+    if page not in PAGE_SIZES or heads != NUM_KV_HEADS or dim != HEAD_DIM:
         raise ValueError("kpages must be [num_pages, 16|32|64|128, 8, 64], got %s"
                          % (tuple(shape),))
     if vpages.dtype is not dtype:
         raise TypeError("vpages must be %s, got %s" % (dtype, vpages.dtype))
     if vpages.shape != shape or vpages.stride() != stride:
         raise ValueError("vpages must have the shape and strides of kpages")
-    if stride[3] != 1:
+    sp, st, sh, sd = stride
+    if sd != 1:
         raise ValueError("the pages' elements must be contiguous, got strides %s" % (stride,))
     if kpages.get_device() != index or vpages.get_device() != index:
         raise ValueError("pages are on %s and %s, not on the device of the call"
@@ -546,15 +550,14 @@ def _paged_cache(kpages, vpages, kscales, vscales, index: int) -> _PagedCache:
     if dtype is _BF16:
         if kscales is not None or vscales is not None:
             raise ValueError("bf16 pages take no scales")
-        return _PagedCache(kpages.data_ptr(), vpages.data_ptr(), None, None, stride[0], stride[1],
-                           stride[2], shape[0], shape[1], 0)
+        return _PagedCache(kpages.data_ptr(), vpages.data_ptr(), None, None, sp, st, sh, num, page,
+                           0)
     if kscales is None or vscales is None:
         raise ValueError("float8_e4m3fn pages need kscales and vscales")
-    scales = (shape[0], NUM_KV_HEADS)
+    scales = (num, NUM_KV_HEADS)
     return _PagedCache(kpages.data_ptr(), vpages.data_ptr(),
                        _array(kscales, _F32, scales, "kscales", index),
-                       _array(vscales, _F32, scales, "vscales", index), stride[0], stride[1],
-                       stride[2], shape[0], shape[1], 1)
+                       _array(vscales, _F32, scales, "vscales", index), sp, st, sh, num, page, 1)
 
 
 def _max_pages(table: torch.Tensor) -> int:
@@ -581,7 +584,7 @@ def _call_on(index: int, stream, fn, *args) -> int:
     """fn(*args, stream) with device `index` current, on `stream` or its current one."""
     handle = stream.cuda_stream if stream is not None else \
         torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         return fn(*args, handle)
     with torch.cuda.device(index):
         return fn(*args, handle)
