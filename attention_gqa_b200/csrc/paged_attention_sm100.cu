@@ -75,7 +75,7 @@ struct Smem {
   static constexpr uint32_t kPage = kQExp + NT * kGroup * 4;
   static constexpr uint32_t kBar = kPage + kStages * kPages * 16;
   static constexpr uint32_t kScan = kBar + 2 * kStages * 8;  // 5 + 5 warp sums, slot
-  static constexpr uint32_t kMisc = kScan + 2 * 5 * 8 + sizeof(ScanSlot);
+  static constexpr uint32_t kMisc = kScan + 2 * 5 * 4 + sizeof(ScanSlot);
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
 };
 
@@ -140,15 +140,15 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
   griddep_wait();
   if (threadIdx.x == 0)
     *abort_flag = (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) ? 1 : 0;
-  ScanSlot* slot = reinterpret_cast<ScanSlot*>(smem + L::kScan + 2 * 5 * 8);
+  ScanSlot* slot = reinterpret_cast<ScanSlot*>(smem + L::kScan + 2 * 5 * 4);
   if (!find_chunk<NT, kTile, kThreads>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
-                                       reinterpret_cast<uint64_t*>(smem + L::kScan), slot))
+                                       reinterpret_cast<uint32_t*>(smem + L::kScan), slot))
     return;  // past the call's last chunk
   const bool skip = *abort_flag != 0;
   const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
   if (a.meta && slot->split == 0 && g == 0 && threadIdx.x == 0)
     a.meta[row] = make_int2(slot->part, chunks);
-  const int b = row / a.groups;
+  const int b = sequence_of(a, row);
   const int t0 = (row - b * a.groups) * NT;
   const int len = slot->len;
   const int idx0 = len - a.n + t0;  // index of the row's first token

@@ -49,33 +49,86 @@ __device__ __forceinline__ int length_of(const PagedAttentionArgs& a, int b) {
   return len;
 }
 
+// Sequence of a row.
+__device__ __forceinline__ int sequence_of(const PagedAttentionArgs& a, int row) {
+  return a.groups == 1 ? row : row / a.groups;
+}
+
 template <int NT, int kTile>
 __device__ __forceinline__ int row_tiles(const PagedAttentionArgs& a, int row) {
-  const int b = row / a.groups;
+  const int b = sequence_of(a, row);
   int lo, hi;
   paged_row_range(length_of(a, b), a.n, (row - b * a.groups) * NT, NT, a.window, &lo, &hi);
   return paged_row_tiles(lo, hi, kTile);
 }
 
-__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+// Inclusive sums over the lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const uint64_t u = __shfl_up_sync(0xffffffffu, v, d);
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, d);
     if (lane >= d) v += u;
   }
   return v;
 }
 
+// The rows of one thread: their tiles and chunks. kRows consecutive ones at most. All rows
+// are fewer than kPagedManyRows, so that their chunks, in the low half of a word, and the
+// chunks of cut rows, in its high half, stay below 2^16.
+template <int NT, int kTile, int kRows>
+struct PlanRows {
+  int r0, r1, tiles[kRows], n[kRows];
+  __device__ __forceinline__ uint32_t load(const PagedAttentionArgs& a, int first, int last) {
+    r0 = min(a.rows, first);
+    r1 = min(a.rows, last);
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      tiles[i] = r0 + i < r1 ? row_tiles<NT, kTile>(a, r0 + i) : 0;
+      sum += static_cast<uint32_t>(tiles[i]);
+    }
+    return sum;
+  }
+  // into chunks of so many tiles; their counts
+  __device__ __forceinline__ uint32_t cut(int chunk) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      n[i] = r0 + i < r1 ? paged_row_chunks(tiles[i], chunk) : 0;
+      sum += words(i);
+    }
+    return sum;
+  }
+  // looks for chunk `cid` here, before whose rows lie the counts `at`
+  __device__ __forceinline__ void find(const PagedAttentionArgs& a, int cid, uint32_t at,
+                                       ScanSlot* slot) const {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int split = cid - static_cast<int>(at & 0xFFFFu);
+      if (split >= 0 && split < n[i]) {
+        slot->row = r0 + i;
+        slot->split = split;
+        slot->chunks = n[i];
+        slot->part = static_cast<int>(at >> 16);
+        slot->len = min(max(__ldg(a.len + sequence_of(a, r0 + i)), 0), a.max_len);
+      }
+      at += words(i);
+    }
+  }
+  __device__ __forceinline__ uint32_t words(int i) const {
+    return static_cast<uint32_t>(n[i]) * (n[i] > 1 ? 0x10001u : 1u);
+  }
+};
+
 // Finds chunk `cid` of the call, by all kThreads threads of the CTA; false past the
-// last one. `sums`: two words per warp. Chunks are counted in the low half of the
-// scanned words, those of rows with several in the high half.
+// last one. `sums`: two words per warp.
 //
-// Every CTA begins with this, so it is kept short: where no row is cut, chunks are rows (and
-// a window of 128 over 64 sequences takes 7.4 us, not 8.1); up to 96 rows the first warp does it
-// alone with sums of 32 bits (no row has more than 2^25 tiles, and 96 make fewer than
-// 2^16 chunks); more are spread over all threads.
+// Every CTA begins with this, so it is kept short: where no row is cut, chunks are rows (a
+// window of 128 over 64 sequences takes 7.2 us, not 8.1, and 1024 ragged sequences of up to
+// 1024 bf16 176 us); up to 96 rows the first warp does it alone; more, below 1024, are spread
+// over all threads (1023 of those: 192 us).
 template <int NT, int kTile, int kThreads>
-__device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid, uint64_t* sums,
+__device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid, uint32_t* sums,
                                            ScanSlot* slot) {
   constexpr int kWarps = kThreads / 32;
   const int t = static_cast<int>(threadIdx.x);
@@ -85,121 +138,63 @@ __device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid,
       slot->row = cid;
       slot->split = slot->part = 0;
       slot->chunks = 1;
-      slot->len = length_of(a, cid / a.groups);
+      slot->len = length_of(a, sequence_of(a, cid));
     }
     __syncthreads();
     return true;  // the grid has no more
   }
+  if (t == 0) slot->row = -1;
   constexpr int kFew = 3;
   if (a.rows <= 32 * kFew) {
     if (warp == 0) {
       const int per = (a.rows + 31) / 32;
-      const int r0 = lane * per, r1 = min(a.rows, r0 + per);
-      if (lane == 0) slot->row = -1;
-      __syncwarp();
-      int tiles[kFew];
-      uint32_t mine = 0;
-#pragma unroll
-      for (int i = 0; i < kFew; ++i) {
-        tiles[i] = r0 + i < r1 ? row_tiles<NT, kTile>(a, r0 + i) : 0;
-        mine += static_cast<uint32_t>(tiles[i]);
-      }
-      const uint32_t total = __reduce_add_sync(0xffffffffu, mine);
-      int n[kFew];
-      int count;
-      auto cut = [&](int chunk) {  // into chunks of so many tiles
-        mine = 0;
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-          n[i] = r0 + i < r1 ? paged_row_chunks(tiles[i], chunk) : 0;
-          mine += static_cast<uint32_t>(n[i]) * (n[i] > 1 ? 0x10001u : 1u);
-        }
-        count = static_cast<int>(__reduce_add_sync(0xffffffffu, mine & 0xFFFFu));
-      };
+      PlanRows<NT, kTile, kFew> rows;
+      const uint32_t total =
+          __reduce_add_sync(0xffffffffu, rows.load(a, lane * per, lane * per + per));
       int chunk = paged_chunk_tiles(total, a.target);
-      cut(chunk);
-      if (a.one_wave) {
+      uint32_t mine = rows.cut(chunk);
+      if (a.one_wave || NT > 2) {
+        int count = static_cast<int>(__reduce_add_sync(0xffffffffu, mine & 0xFFFFu));
         // (ends: chunks grow until every row is one, and the rows are fewer than a wave)
-        while (count > a.wave) cut(chunk = paged_longer_chunk(chunk, count, a.wave));
-      } else if constexpr (NT > 2) {
-        int tail = 0, whole = 0;
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-          if (n[i] > 0) tail = max(tail, (tiles[i] + n[i] - 1) / n[i]);
-          whole = max(whole, tiles[i]);
+        while (a.one_wave && count > a.wave) {
+          chunk = paged_longer_chunk(chunk, count, a.wave);
+          mine = rows.cut(chunk);
+          count = static_cast<int>(__reduce_add_sync(0xffffffffu, mine & 0xFFFFu));
         }
-        tail = __reduce_max_sync(0xffffffffu, tail);
-        whole = __reduce_max_sync(0xffffffffu, whole);
-        if (paged_estimate(total, a.rows, whole, a.wave, false) <=
-            paged_estimate(total, count, tail, a.wave, true))
-          cut(whole);
-      }
-      uint32_t at = mine;
+        if (!a.one_wave) {
+          int longest = 0, whole = 0;
 #pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, at, d);
-        if (lane >= d) at += u;
-      }
-      at -= mine;
-#pragma unroll
-      for (int i = 0; i < kFew; ++i) {
-        const int split = cid - static_cast<int>(at & 0xFFFFu);
-        if (split >= 0 && split < n[i]) {
-          slot->row = r0 + i;
-          slot->split = split;
-          slot->chunks = n[i];
-          slot->part = static_cast<int>(at >> 16);
-          slot->len = min(max(__ldg(a.len + (r0 + i) / a.groups), 0), a.max_len);
+          for (int i = 0; i < kFew; ++i) {
+            if (rows.n[i] > 0) longest = max(longest, (rows.tiles[i] + rows.n[i] - 1) / rows.n[i]);
+            whole = max(whole, rows.tiles[i]);
+          }
+          longest = __reduce_max_sync(0xffffffffu, longest);
+          whole = __reduce_max_sync(0xffffffffu, whole);
+          if (paged_estimate(total, a.rows, whole, a.wave, false) <=
+              paged_estimate(total, count, longest, a.wave, true))
+            mine = rows.cut(whole);
         }
-        at += static_cast<uint32_t>(n[i]) * (n[i] > 1 ? 0x10001u : 1u);
       }
+      rows.find(a, cid, warp_scan(mine, lane) - mine, slot);
     }
+  } else {
+    const int per = (a.rows + kThreads - 1) / kThreads;
+    PlanRows<NT, kTile, (kPagedManyRows - 1 + kThreads - 1) / kThreads> rows;
+    const uint32_t part = __reduce_add_sync(0xffffffffu, rows.load(a, t * per, t * per + per));
+    if (lane == 0) sums[warp] = part;
     __syncthreads();
-    return slot->row >= 0;
-  }
-  const int per = (a.rows + kThreads - 1) / kThreads;
-  const int r0 = min(a.rows, t * per), r1 = min(a.rows, r0 + per);
-  if (t == 0) slot->row = -1;
-  int first = 0;
-  uint64_t mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    first = row_tiles<NT, kTile>(a, r);
-    mine += static_cast<uint64_t>(first);
-  }
-  uint64_t inc = warp_scan(mine, lane);
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  uint64_t total = 0;
+    uint32_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sums[w];
-  const int chunk = paged_chunk_tiles(static_cast<int64_t>(total), a.target);
-
-  mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    const uint64_t n = paged_row_chunks(per == 1 ? first : row_tiles<NT, kTile>(a, r), chunk);
-    mine += n | (n > 1 ? n << 32 : 0);
-  }
-  inc = warp_scan(mine, lane);
-  if (lane == 31) sums[kWarps + warp] = inc;
-  __syncthreads();
-  uint64_t at = inc - mine;
+    for (int w = 0; w < kWarps; ++w) total += sums[w];
+    const uint32_t mine = rows.cut(paged_chunk_tiles(total, a.target));
+    const uint32_t inc = warp_scan(mine, lane);
+    if (lane == 31) sums[kWarps + warp] = inc;
+    __syncthreads();
+    uint32_t at = inc - mine;
 #pragma unroll
-  for (int w = 0; w < kWarps - 1; ++w)
-    if (w < warp) at += sums[kWarps + w];
-  if (static_cast<uint32_t>(cid) - static_cast<uint32_t>(at) < static_cast<uint32_t>(mine)) {
-    for (int r = r0; r < r1; ++r) {
-      const int n = paged_row_chunks(per == 1 ? first : row_tiles<NT, kTile>(a, r), chunk);
-      const int i = cid - static_cast<int>(static_cast<uint32_t>(at));
-      if (i < n) {
-        slot->row = r;
-        slot->split = i;
-        slot->chunks = n;
-        slot->part = static_cast<int>(at >> 32);
-        slot->len = min(max(__ldg(a.len + r / a.groups), 0), a.max_len);
-        break;
-      }
-      at += static_cast<uint64_t>(n) | (n > 1 ? static_cast<uint64_t>(n) << 32 : 0);
-    }
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < warp) at += sums[kWarps + w];
+    rows.find(a, cid, at, slot);
   }
   __syncthreads();
   return slot->row >= 0;

@@ -77,7 +77,7 @@ struct Smem {
   static constexpr uint32_t kBad = kBar + 32 * 8;  // [2][2][4] value rows taken out of a tile
   static constexpr uint32_t kHalfBytes = (kBad + 64 + 1023) / 1024 * 1024;
   static constexpr uint32_t kScan = 2 * kHalfBytes;  // 16 + 16 warp sums, slot
-  static constexpr uint32_t kMisc = kScan + 32 * 8 + sizeof(ScanSlot);  // abort flag, TMEM address
+  static constexpr uint32_t kMisc = kScan + 32 * 4 + sizeof(ScanSlot);  // abort flag, TMEM address
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
 };
 static_assert(Smem<false>::kBytes <= 227 * 1024 && Smem<true>::kBytes <= 227 * 1024, "shared memory");
@@ -242,15 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   if (threadIdx.x == 0)
     *ctx.abort_flag = (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) ? 1 : 0;
-  ScanSlot* slot = reinterpret_cast<ScanSlot*>(cta_smem + L::kScan + 32 * 8);
+  ScanSlot* slot = reinterpret_cast<ScanSlot*>(cta_smem + L::kScan + 32 * 4);
   if (!find_chunk<kNT, kTile, kThreads>(a, static_cast<int>(blockIdx.x / kCtas),
-                                        reinterpret_cast<uint64_t*>(cta_smem + L::kScan), slot))
+                                        reinterpret_cast<uint32_t*>(cta_smem + L::kScan), slot))
     return;  // past the call's last chunk
   const bool skip = *ctx.abort_flag != 0;
   const int row = slot->row, chunks = slot->chunks, part = slot->part + slot->split;
   if (a.meta && slot->split == 0 && g == 0 && threadIdx.x == 0)
     a.meta[row] = make_int2(slot->part, chunks);
-  const int b = row / a.groups;
+  const int b = sequence_of(a, row);
   const int t0 = (row - b * a.groups) * kNT;
   const int len = slot->len;
   const int idx0 = len - a.n + t0;  // index of the row's first token
