@@ -11,9 +11,9 @@
 //
 // Both kernels have HBM's floor: 256 bytes read per token and kv head, 256 (bf16) or 128
 // (e4m3) written. Measured on a B200 for 4 x 16384 tokens: bf16 43.3 us, 6.2 TB/s of that;
-// e4m3 57.4 us, 3.5 TB/s, its CTAs waiting in turn for their tokens and for their largest
-// value (the issue slots are 56 % used, and 64 registers a thread allow two CTAs of 512
-// per SM). One token of 64 sequences: 1.7 and 2.6 us on the device, less than a launch.
+// e4m3 55 us, 3.7 TB/s, whose CTAs wait in turn for their tokens and for their largest value
+// (64 registers a thread allow 32 warps per SM, and half of the issue slots are used). One
+// token of 64 sequences: 1.7 and 2.6 us on the device, less than a launch.
 #include "internal.h"
 #include "paged.h"
 #include "sm100_ptx.cuh"
@@ -188,31 +188,32 @@ __device__ __forceinline__ float largest_finite(const Halves& x, float top) {
 
 constexpr int kAppendWarps = 16;  // most warps of a CTA
 
-// Two CTAs per page that a sequence's new tokens touch, one for its keys and one for its
-// values. A warp takes every W-th new token of the page, all heads of it, four lanes
-// a head as above (1 KB per load, and one table row for all heads); kTokens is how
-// many that can be. Tokens are read once and kept (the first four; a warp has more only
-// in pages of 128), for the largest value of each head, over the CTA, and then for
-// the codes. Tried for those 4 x 16384 tokens (57.4 us): a warp per (page, head) that reads
-// twice, 90 us; one CTA for a page's keys and values, 63 to 70; 256 threads with half of
-// the tokens read again, 60.6; 40 registers and three CTAs, 69.
+// Four CTAs per page that a sequence's new tokens touch, for half of the heads of its keys
+// and of its values each: the scale needs the largest of all the page's new values, and the
+// smaller the CTA that waits for them, the better its waits pass under others' work. Half a
+// warp takes a token, four lanes a head as above (512 bytes in a row); the tokens of the
+// warps, at most kTokens to a lane, are read once and kept, for the largest value of each
+// head over the CTA and then for the codes. For 4 x 16384 tokens in pages of 16, 32, 64 and
+// 128: 52, 51, 55 and 61 us; with all heads in a CTA 81, 60, 57 and 65 us; with keys and
+// values in one, 63 to 70 (64); a warp per (page, head) that reads twice, 90 (64).
 template <int kTokens>
 __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     append_e4m3_kernel(const PagedAppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kKeep = kTokens < 4 ? kTokens : 4;
-  __shared__ float tops[kAppendWarps][kNumKvHeads];
+  __shared__ float tops[kAppendWarps][kNumKvHeads / 2];
   const int b = static_cast<int>(blockIdx.y);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int warps = static_cast<int>(blockDim.x >> 5);
-  const int head = lane >> 2, c = lane & 3;
-  const bool is_v = (blockIdx.x & 1) != 0;
+  const int sub = lane >> 4;  // which token of the warp's two
+  const int local = (lane >> 2) & 3, c = lane & 3;
+  const int head = local + 4 * static_cast<int>(blockIdx.x & 1);
+  const bool is_v = (blockIdx.x & 2) != 0;
   int start, count;
   if (!new_tokens(a, b, &start, &count)) return;
   const PagedCache& pc = a.cache;
   const int P = 1 << pc.page_log2;
-  const int pi = (start >> pc.page_log2) + static_cast<int>(blockIdx.x >> 1);  // of the sequence
+  const int pi = (start >> pc.page_log2) + static_cast<int>(blockIdx.x >> 2);  // of the sequence
   const int base = pi << pc.page_log2;  // the page's first index
   if (base >= start + count) return;
   const int s0 = start > base ? start - base : 0;  // slots [s0, s1) are new
@@ -222,7 +223,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   const uint16_t* src = (is_v ? a.v + b * a.v_batch : a.k + b * a.k_batch) + head * kHeadDim;
   const int64_t src_token = is_v ? a.v_token : a.k_token;
 
-  uint4 keep[kKeep][2];  // this lane's chunks c and c+4
+  uint4 keep[kTokens][2];  // this lane's chunks c and c+4
+  const int mine = s0 + 2 * warp + sub;  // its first slot; the others 2 * warps apart
   auto load = [&](int s, uint4 (&w)[2]) {
     const uint4* p4 = reinterpret_cast<const uint4*>(src + (t0 + s) * src_token);
     w[0] = __ldg(p4 + c);
@@ -243,17 +245,15 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     return x;
   };
 #pragma unroll
-  for (int i = 0; i < kKeep; ++i)
-    if (s0 + warp + i * warps < s1) load(s0 + warp + i * warps, keep[i]);
+  for (int i = 0; i < kTokens; ++i)
+    if (mine + 2 * i * warps < s1) load(mine + 2 * i * warps, keep[i]);
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    const int s = s0 + warp + i * warps;
+    const int s = mine + 2 * i * warps;
     if (s >= s1) break;
-    uint4 more[2];
-    if (i >= kKeep) load(s, more);
     // an ulp on the largest value makes no difference to the codes
-    const Halves x = value(s, i < kKeep ? keep[i < kKeep ? i : 0] : more, false);
+    const Halves x = value(s, keep[i], false);
     const float all = largest(x, top);
     top = all < INFINITY ? all : largest_finite(x, top);
   }
@@ -263,23 +263,24 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
   // the scale that the page has, if it holds earlier tokens
   float* scale = (is_v ? pc.v_scale : pc.k_scale) + static_cast<int64_t>(page) * kNumKvHeads + head;
   const float before = s0 > 0 ? *scale : 0.f;
   if (warps > 1) {
-    if (c == 0) tops[warp][head] = top;
+    if (c == 0 && sub == 0) tops[warp][local] = top;
     __syncthreads();  // and every warp has read the scale
-    for (int w = 0; w < warps; ++w) top = fmaxf(top, tops[w][head]);
+    for (int w = 0; w < warps; ++w) top = fmaxf(top, tops[w][local]);
   }
   __syncwarp();
   const float least = __uint_as_float(paged_scale_bits(__float_as_uint(top)));
   const float size = before >= least ? before : least;
-  if (warp == 0 && c == 0) *scale = size;
+  if (warp == 0 && c == 0 && sub == 0) *scale = size;
   uint8_t* dst = (is_v ? pc.v : pc.k) + page * pc.page_stride + head * pc.head_stride;
   if (size != before) {
     // it grew (for this lane's head): move the earlier tokens' codes
     const float f = before / size;
-    for (int s = warp; s < s0; s += warps) {
+    for (int s = 2 * warp + sub; s < s0; s += 2 * warps) {
       uint4* row4 = reinterpret_cast<uint4*>(dst + s * pc.token_stride) + c;
       const uint4 w = *row4;
       *row4 = make_uint4(move_e4m3x4(w.x, f), move_e4m3x4(w.y, f), move_e4m3x4(w.z, f),
@@ -289,11 +290,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   const float inv = 1.f / size;
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    const int s = s0 + warp + i * warps;
+    const int s = mine + 2 * i * warps;
     if (s >= s1) break;
-    uint4 more[2];
-    if (i >= kKeep) load(s, more);
-    const Halves x = value(s, i < kKeep ? keep[i < kKeep ? i : 0] : more, true);
+    const Halves x = value(s, keep[i], true);
     uint2* row2 = reinterpret_cast<uint2*>(dst + s * pc.token_stride);
     row2[c] = pack_e4m3x8(x.lo, inv);
     row2[c + 4] = pack_e4m3x8(x.hi, inv);
@@ -314,15 +313,20 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
     // pages that n tokens can touch, wherever in a page they start
     const int P = 1 << a.cache.page_log2;
     const int most = a.n < P ? a.n : P;  // new tokens in one page
+    const unsigned pages = static_cast<unsigned>((a.n + P - 2) / P + 1);
+    // Two tokens to a lane while all warps fit the GPU at once (32 to an SM), four beyond
+    // (2 x 2048 in pages of 64: 6.2 and 8.5 us; 4 x 16384: 65 and 55).
     int warps = 1;
-    while (warps < kAppendWarps && warps < most) warps *= 2;
-    cfg.gridDim = dim3(2 * static_cast<unsigned>((a.n + P - 2) / P + 1),
-                       static_cast<unsigned>(a.batch));
+    while (warps < kAppendWarps && 4 * warps < most) warps *= 2;
+    if (warps > 1 && static_cast<int64_t>(pages) * a.batch * 4 * warps > 148 * 32) {
+      warps = 1;
+      while (warps < kAppendWarps && 8 * warps < most) warps *= 2;
+    }
+    cfg.gridDim = dim3(4 * pages, static_cast<unsigned>(a.batch));
     cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
-    if (most <= warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<1>, a);
-    if (most <= 2 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<2>, a);
-    if (most <= 4 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<4>, a);
-    return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<8>, a);
+    if (most <= 2 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<1>, a);
+    if (most <= 4 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<2>, a);
+    return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<4>, a);
   }
   int warps = 1;
   while (warps < 8 && warps < a.n) warps *= 2;
