@@ -11,7 +11,7 @@
 //
 // Both kernels have HBM's floor: 256 bytes read per token and kv head, 256 (bf16) or 128
 // (e4m3) written. Measured on a B200 for 4 x 16384 tokens: bf16 43.3 us, 6.2 TB/s of that;
-// e4m3 55 us, 3.7 TB/s, whose CTAs wait in turn for their tokens and for their largest value
+// e4m3 52 us, 3.9 TB/s, whose CTAs wait in turn for their tokens and for their largest value
 // (64 registers a thread allow 32 warps per SM, and half of the issue slots are used). One
 // token of 64 sequences: 1.7 and 2.6 us on the device, less than a launch.
 #include "internal.h"
@@ -188,32 +188,33 @@ __device__ __forceinline__ float largest_finite(const Halves& x, float top) {
 
 constexpr int kAppendWarps = 16;  // most warps of a CTA
 
-// Four CTAs per page that a sequence's new tokens touch, for half of the heads of its keys
-// and of its values each: the scale needs the largest of all the page's new values, and the
-// smaller the CTA that waits for them, the better its waits pass under others' work. Half a
-// warp takes a token, four lanes a head as above (512 bytes in a row); the tokens of the
-// warps, at most kTokens to a lane, are read once and kept, for the largest value of each
-// head over the CTA and then for the codes. For 4 x 16384 tokens in pages of 16, 32, 64 and
-// 128: 52, 51, 55 and 61 us; with all heads in a CTA 81, 60, 57 and 65 us; with keys and
-// values in one, 63 to 70 (64); a warp per (page, head) that reads twice, 90 (64).
+// Eight CTAs per page that a sequence's new tokens touch, for two heads of its keys or of its
+// values each: the scale needs the largest of all the page's new values, and the smaller
+// the CTA that waits for them, the better its waits pass under others' work. Eight lanes
+// take a token, four a head as above (256 bytes in a row); a warp's tokens, at most kTokens to
+// a lane, are read once and kept, for the largest value of each head over the CTA and
+// then for the codes. For 4 x 16384 tokens in pages of 16, 32, 64 and 128: 52, 53, 52 and 56
+// us; with four heads in a CTA 51, 50, 54 and 61; with eight 81, 60, 57 and 65; with keys and
+// values in one, 63 to 70 (64); a warp per (page, head) that reads twice, 90 (64). For 7 x
+// 333 in pages of 128: 6.0 us; with four heads 8.3, with eight 13.9.
 template <int kTokens>
 __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     append_e4m3_kernel(const PagedAppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ float tops[kAppendWarps][kNumKvHeads / 2];
+  __shared__ float tops[kAppendWarps][2];  // by warp and head
   const int b = static_cast<int>(blockIdx.y);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int warps = static_cast<int>(blockDim.x >> 5);
-  const int sub = lane >> 4;  // which token of the warp's two
-  const int local = (lane >> 2) & 3, c = lane & 3;
-  const int head = local + 4 * static_cast<int>(blockIdx.x & 1);
-  const bool is_v = (blockIdx.x & 2) != 0;
+  const int sub = lane >> 3;  // which token of the warp's four
+  const int local = (lane >> 2) & 1, c = lane & 3;
+  const int head = local + 2 * static_cast<int>(blockIdx.x & 3);
+  const bool is_v = (blockIdx.x & 4) != 0;
   int start, count;
   if (!new_tokens(a, b, &start, &count)) return;
   const PagedCache& pc = a.cache;
   const int P = 1 << pc.page_log2;
-  const int pi = (start >> pc.page_log2) + static_cast<int>(blockIdx.x >> 2);  // of the sequence
+  const int pi = (start >> pc.page_log2) + static_cast<int>(blockIdx.x >> 3);  // of the sequence
   const int base = pi << pc.page_log2;  // the page's first index
   if (base >= start + count) return;
   const int s0 = start > base ? start - base : 0;  // slots [s0, s1) are new
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   const int64_t src_token = is_v ? a.v_token : a.k_token;
 
   uint4 keep[kTokens][2];  // this lane's chunks c and c+4
-  const int mine = s0 + 2 * warp + sub;  // its first slot; the others 2 * warps apart
+  const int mine = s0 + 4 * warp + sub;  // its first slot; the others 4 * warps apart
   auto load = [&](int s, uint4 (&w)[2]) {
     const uint4* p4 = reinterpret_cast<const uint4*>(src + (t0 + s) * src_token);
     w[0] = __ldg(p4 + c);
@@ -246,11 +247,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   };
 #pragma unroll
   for (int i = 0; i < kTokens; ++i)
-    if (mine + 2 * i * warps < s1) load(mine + 2 * i * warps, keep[i]);
+    if (mine + 4 * i * warps < s1) load(mine + 4 * i * warps, keep[i]);
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    const int s = mine + 2 * i * warps;
+    const int s = mine + 4 * i * warps;
     if (s >= s1) break;
     // an ulp on the largest value makes no difference to the codes
     const Halves x = value(s, keep[i], false);
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
   // the scale that the page has, if it holds earlier tokens
   float* scale = (is_v ? pc.v_scale : pc.k_scale) + static_cast<int64_t>(page) * kNumKvHeads + head;
   const float before = s0 > 0 ? *scale : 0.f;
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   if (size != before) {
     // it grew (for this lane's head): move the earlier tokens' codes
     const float f = before / size;
-    for (int s = 2 * warp + sub; s < s0; s += 2 * warps) {
+    for (int s = 4 * warp + sub; s < s0; s += 4 * warps) {
       uint4* row4 = reinterpret_cast<uint4*>(dst + s * pc.token_stride) + c;
       const uint4 w = *row4;
       *row4 = make_uint4(move_e4m3x4(w.x, f), move_e4m3x4(w.y, f), move_e4m3x4(w.z, f),
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   const float inv = 1.f / size;
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    const int s = mine + 2 * i * warps;
+    const int s = mine + 4 * i * warps;
     if (s >= s1) break;
     const Halves x = value(s, keep[i], true);
     uint2* row2 = reinterpret_cast<uint2*>(dst + s * pc.token_stride);
@@ -315,17 +317,17 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
     const int most = a.n < P ? a.n : P;  // new tokens in one page
     const unsigned pages = static_cast<unsigned>((a.n + P - 2) / P + 1);
     // Two tokens to a lane while all warps fit the GPU at once (32 to an SM), four beyond
-    // (2 x 2048 in pages of 64: 6.2 and 8.5 us; 4 x 16384: 65 and 55).
+    // (four heads in a CTA: 2 x 2048 in pages of 64 6.2 and 8.5 us, 4 x 16384 65 and 55).
     int warps = 1;
-    while (warps < kAppendWarps && 4 * warps < most) warps *= 2;
-    if (warps > 1 && static_cast<int64_t>(pages) * a.batch * 4 * warps > 148 * 32) {
+    while (warps < kAppendWarps && 8 * warps < most) warps *= 2;
+    if (warps > 1 && static_cast<int64_t>(pages) * a.batch * 8 * warps > 148 * 32) {
       warps = 1;
-      while (warps < kAppendWarps && 8 * warps < most) warps *= 2;
+      while (warps < kAppendWarps && 16 * warps < most) warps *= 2;
     }
-    cfg.gridDim = dim3(4 * pages, static_cast<unsigned>(a.batch));
+    cfg.gridDim = dim3(8 * pages, static_cast<unsigned>(a.batch));
     cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
-    if (most <= 2 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<1>, a);
-    if (most <= 4 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<2>, a);
+    if (most <= 4 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<1>, a);
+    if (most <= 8 * warps) return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<2>, a);
     return cudaLaunchKernelEx(&cfg, append_e4m3_kernel<4>, a);
   }
   int warps = 1;
