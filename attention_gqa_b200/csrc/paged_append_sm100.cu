@@ -7,13 +7,17 @@
 // and head, a power of two so that a later, larger scale moves the codes that
 // are there without rounding them again (but for those that get subnormal):
 //   s = max(s of the page's earlier tokens, least 2^e with max |x| <= 448 * 2^e).
-// Infinities saturate and NaN stays; neither decides the scale.
+// Infinities saturate and NaN stays; neither decides the scale. A rotation may pass fp32's
+// range (bf16's largest, times sqrt 2 and YaRN's factor); what it gives is finite all the same.
 //
 // Both kernels have HBM's floor: 256 bytes read per token and kv head, 256 (bf16) or 128
 // (e4m3) written. Measured on a B200 for 4 x 16384 tokens: bf16 43.3 us, 6.2 TB/s of that;
 // e4m3 52 us, 3.9 TB/s, whose CTAs wait in turn for their tokens and for their largest value
 // (64 registers a thread allow 32 warps per SM, and half of the issue slots are used). One
 // token of 64 sequences: 1.7 and 2.6 us on the device, less than a launch.
+#include <cfloat>
+#include <cmath>
+
 #include "internal.h"
 #include "paged.h"
 #include "sm100_ptx.cuh"
@@ -170,23 +174,17 @@ __device__ __forceinline__ uint32_t move_e4m3x4(uint32_t codes, float f) {
   return pack_e4m3x2(a.x * f, a.y * f) | pack_e4m3x2(b.x * f, b.y * f) << 16;
 }
 
-// The largest |value|, NaN aside; infinite if there is an infinity.
+// The largest |value|, NaN aside; infinite if there is an infinity, or a sum beyond fp32's range.
 __device__ __forceinline__ float largest(const Halves& x, float top) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = fmax3(top, fabsf(x.lo[e]), fabsf(x.hi[e]));
   return top;
 }
 
-__device__ __forceinline__ float largest_finite(const Halves& x, float top) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float u = fabsf(x.lo[e]), v = fabsf(x.hi[e]);
-    top = fmax3(top, u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f);
-  }
-  return top;
-}
-
 constexpr int kAppendWarps = 16;  // most warps of a CTA
+// Below this no product or sum of a rotation overflows fp32, nor does an infinity hide: one
+// element of a pair at least is infinite if an input was.
+constexpr float kWide = 0x1p127f;
 
 // Eight CTAs per page that a sequence's new tokens touch, for two heads of its keys or of its
 // values each: the scale needs the largest of all the page's new values, and the smaller
@@ -245,6 +243,23 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     }
     return x;
   };
+  // The same in 64 bits, this lane's pairs one after the other: products of a bf16 and a table
+  // entry are exact there and overflow nothing, so only an infinite element gives an infinity.
+  // (As rare as it is slow; it reads the token again, to leave the others their registers.)
+  auto each_pair = [&](int s, auto&& use) {
+    const uint16_t* x = src + (t0 + s) * src_token + 8 * c;
+    const float2* row = is_v ? nullptr : table_row(a, b, t0 + s) + 8 * c;
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const double lo = bf16lo_to_f32(__ldg(x + e)), hi = bf16lo_to_f32(__ldg(x + e + 32));
+      if (is_v) {
+        use(e, lo, hi);
+      } else {
+        const float2 f = __ldg(row + e);
+        use(e, lo * f.x - hi * f.y, hi * f.x + lo * f.y);
+      }
+    }
+  };
 #pragma unroll
   for (int i = 0; i < kTokens; ++i)
     if (mine + 4 * i * warps < s1) load(mine + 4 * i * warps, keep[i]);
@@ -254,9 +269,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     const int s = mine + 4 * i * warps;
     if (s >= s1) break;
     // an ulp on the largest value makes no difference to the codes
-    const Halves x = value(s, keep[i], false);
-    const float all = largest(x, top);
-    top = all < INFINITY ? all : largest_finite(x, top);
+    top = largest(value(s, keep[i], false), top);
+  }
+  const bool wide = !(top < kWide);
+  if (wide) {
+    top = 0.f;
+#pragma unroll 1
+    for (int s = mine; s < s1; s += 4 * warps)
+      each_pair(s, [&](int, double lo, double hi) {
+        // a value past fp32's range counts as fp32's largest: both take the largest scale
+        if (fabs(lo) < HUGE_VAL) top = fmaxf(top, fminf(static_cast<float>(fabs(lo)), FLT_MAX));
+        if (fabs(hi) < HUGE_VAL) top = fmaxf(top, fminf(static_cast<float>(fabs(hi)), FLT_MAX));
+      });
   }
   if (!paged_page_ok(page, pc.num_pages)) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrPage);
@@ -290,6 +314,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     }
   }
   const float inv = 1.f / size;
+  if (wide) {
+#pragma unroll 1
+    for (int s = mine; s < s1; s += 4 * warps)
+      each_pair(s, [&](int e, double lo, double hi) {
+        uint8_t* at = dst + s * pc.token_stride + 8 * c + e;
+        const uint32_t codes =
+            pack_e4m3x2(static_cast<float>(lo * inv), static_cast<float>(hi * inv));
+        at[0] = static_cast<uint8_t>(codes);
+        at[32] = static_cast<uint8_t>(codes >> 8);
+      });
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     const int s = mine + 4 * i * warps;

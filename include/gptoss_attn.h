@@ -359,7 +359,8 @@ typedef struct gptoss_attn_paged_cache {
  * every new finite |value| <= 448 * 2^e, or the scale that the page has, if it holds
  * earlier tokens of the sequence and that is larger; if it is smaller, the
  * codes of those tokens are moved to the new scale (exact but for values that
- * become subnormal). Infinities saturate; NaN stays NaN. A page that gets its
+ * become subnormal). Infinities saturate; NaN stays NaN. (A rotated key past fp32's
+ * range is a finite value: what exceeds 448 * 2^120 saturates.) A page that gets its
  * slot 0 in this call forgets the scale that it had. A page that two sequences
  * share must not take new tokens. Slots at or past len[b] are left as they are.
  * A sequence with count[b] outside [0, n] or len[b] outside [count[b],
