@@ -122,4 +122,10 @@ GQA_HD uint32_t paged_scale_bits(uint32_t largest_bits) {
   return static_cast<uint32_t>(e + 127) << 23;
 }
 
+// Whether a value (bits of a finite fp32 >= 0) lies within 16 ulps of where its scale
+// changes, 1.75 * 2^x.
+GQA_HD bool paged_near_border(uint32_t bits) {
+  return (bits & 0x7FFFFFu) - (0x600000u - 16u) <= 32u;
+}
+
 }  // namespace gqa

@@ -268,35 +268,49 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 2)
   for (int i = 0; i < kTokens; ++i) {
     const int s = mine + 4 * i * warps;
     if (s >= s1) break;
-    // an ulp on the largest value makes no difference to the codes
+    // (with the cheaper rotation, which is off by two or three ulps of the page's largest value)
     top = largest(value(s, keep[i], false), top);
   }
   const bool wide = !(top < kWide);
-  if (wide) {
-    top = 0.f;
+  // the largest finite value of this lane's tokens itself, in fp32
+  auto exact_top = [&] {
+    float t = 0.f;
 #pragma unroll 1
     for (int s = mine; s < s1; s += 4 * warps)
       each_pair(s, [&](int, double lo, double hi) {
         // a value past fp32's range counts as fp32's largest: both take the largest scale
-        if (fabs(lo) < HUGE_VAL) top = fmaxf(top, fminf(static_cast<float>(fabs(lo)), FLT_MAX));
-        if (fabs(hi) < HUGE_VAL) top = fmaxf(top, fminf(static_cast<float>(fabs(hi)), FLT_MAX));
+        if (fabs(lo) < HUGE_VAL) t = fmaxf(t, fminf(static_cast<float>(fabs(lo)), FLT_MAX));
+        if (fabs(hi) < HUGE_VAL) t = fmaxf(t, fminf(static_cast<float>(fabs(hi)), FLT_MAX));
       });
-  }
+    return t;
+  };
   if (!paged_page_ok(page, pc.num_pages)) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrPage);
     return;
   }
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+  // the largest of a head over the CTA, in every lane of the head
+  auto of_page = [&](float t) {
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+    if (warps > 1) {
+      if (c == 0 && sub == 0) tops[warp][local] = t;
+      __syncthreads();  // and, the first time, every warp has read the scale
+      for (int w = 0; w < warps; ++w) t = fmaxf(t, tops[w][local]);
+    }
+    return t;
+  };
   // the scale that the page has, if it holds earlier tokens
   float* scale = (is_v ? pc.v_scale : pc.k_scale) + static_cast<int64_t>(page) * kNumKvHeads + head;
   const float before = s0 > 0 ? *scale : 0.f;
-  if (warps > 1) {
-    if (c == 0 && sub == 0) tops[warp][local] = top;
-    __syncthreads();  // and every warp has read the scale
-    for (int w = 0; w < warps; ++w) top = fmaxf(top, tops[w][local]);
+  top = of_page(top);
+  // At a border the two rotations may lie on two sides. (Every warp has both heads' lanes, so
+  // the whole CTA comes here or none does.)
+  const bool again = !(top < kWide) || (!is_v && paged_near_border(__float_as_uint(top)));
+  if (__any_sync(0xffffffffu, again)) {
+    if (warps > 1) __syncthreads();
+    top = of_page(exact_top());
   }
   __syncwarp();
   const float least = __uint_as_float(paged_scale_bits(__float_as_uint(top)));

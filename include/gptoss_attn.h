@@ -356,7 +356,8 @@ typedef struct gptoss_attn_paged_cache {
  *           of k, v and pos past count[b] are not used
  * bf16 pages hold exactly what gptoss_attn_prefill_chunk() would write. e4m3 pages:
  * per (page, head), the scale is the least power of two 2^e, -64 <= e <= 120, with
- * every new finite |value| <= 448 * 2^e, or the scale that the page has, if it holds
+ * every new finite |value| <= 448 * 2^e (rotated keys as exact products with the fp32
+ * rotary table, rounded to fp32), or the scale that the page has, if it holds
  * earlier tokens of the sequence and that is larger; if it is smaller, the
  * codes of those tokens are moved to the new scale (exact but for values that
  * become subnormal). Infinities saturate; NaN stays NaN. (A rotated key past fp32's

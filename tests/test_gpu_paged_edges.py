@@ -75,3 +75,36 @@ def test_infinite_and_huge_keys(cuda_device, rope, n, page):
     for b in range(B):
         _check_codes(cache, b, n, turned[b], 2.0 ** -21 * 1.4 * mag[b], cache.ks, cache.k, (b, "k"))
         _check_codes(cache, b, n, kf[b], 0.0 * mag[b], cache.vs, cache.v, (b, "v"))
+
+
+@pytest.mark.parametrize("n,page", [(1, 16), (9, 16), (128, 128)])
+def test_a_scale_at_a_border_follows_the_value_itself(cuda_device, n, page):
+    """Keys (position, pair, a, b) whose a cos - b sin lies within two fp32 steps of 448, where
+    a rotation with a rounded product comes out on the other side: the scale is
+    the least that holds the value, which 64 bits and fp32's table and nearest rounding agree on."""
+    cases = [(42766, 29, -180.0, 434.0, True), (83011, 1, 576.0, 23.0, True),
+             (6688, 29, 402.0, -366.0, True), (104611, 30, -238.0, 426.0, True),
+             (127121, 13, -79.0, 458.0, True), (29667, 9, -234.0, -386.0, False),
+             (122418, 17, -188.0, 410.0, False), (92642, 21, -229.0, -486.0, False)]
+    B = 8
+    g = torch.Generator().manual_seed(32)
+    k = torch.randn(B, n, 8, 64, generator=g)
+    pos = torch.zeros(B, n, dtype=torch.int32)
+    for b in range(B):
+        for h in range(8):
+            p, pair, x, y, _ = cases[b]
+            t = (5 * h) % n
+            pos[b] = p
+            e = 2.0 ** ((7 * h) % 11 - 5)
+            k[b, t, h, pair], k[b, t, h, pair + 32] = e * x, e * y
+    k = k.to(torch.bfloat16).cuda()
+    cache = Cache([n] * B, page, E4M3, stale=0.0)
+    gqa.paged_append(k, k, pos.cuda(), cache.k, cache.v, cache.table, _int([n] * B), **cache.scales())
+    gqa.check()
+    for b, (p, pair, x, y, above) in enumerate(cases):
+        got = _f64(cache.ks[int(cache.table_host[b, 0])])
+        e = np.array([2.0 ** ((7 * h) % 11 - 5) for h in range(8)])
+        unit = np.eye(64)
+        value = abs(_rotate((x * unit[pair] + y * unit[pair + 32])[None], p, "plain")[0, pair])
+        assert (value > 448.0) == above and abs(value - 448.0) < 2.0 ** -14
+        assert np.array_equal(got, e * (2.0 if above else 1.0)), (b, got / e)
