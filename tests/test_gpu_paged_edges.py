@@ -108,3 +108,50 @@ def test_a_scale_at_a_border_follows_the_value_itself(cuda_device, n, page):
         value = abs(_rotate((x * unit[pair] + y * unit[pair + 32])[None], p, "plain")[0, pair])
         assert (value > 448.0) == above and abs(value - 448.0) < 2.0 ** -14
         assert np.array_equal(got, e * (2.0 if above else 1.0)), (b, got / e)
+
+
+@pytest.mark.parametrize("rope", ["plain", "yarn"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_scales_of_rotated_keys_and_of_pages_used_before(cuda_device, page, rope):
+    """Every touched page's scale is the least that holds its new tokens, or the one that its
+    earlier tokens had if that is larger; what an earlier owner left in a page counts for
+    nothing once the page gets its first slot."""
+    lengths = [1, page, page + 1, 2 * page + 5, 300, 301, 3 * page, 7]
+    counts = [1, page, 1, page + 9, 150, 7, 3 * page, 0]
+    B, n = len(lengths), max(counts)
+    starts = [a - c for a, c in zip(lengths, counts)]
+    g = torch.Generator().manual_seed(90 + page)
+    cache = Cache(lengths, page, E4M3)
+    cache.ks.fill_(2.0 ** 40)
+    cache.vs.fill_(2.0 ** 40)
+    cache.fill(starts, g)
+    before = cache.ks.clone(), cache.vs.clone()
+    size = torch.exp(2.0 * torch.randn(B, n, 8, 1, generator=g))
+    k = (size * torch.randn(B, n, 8, 64, generator=g)).to(torch.bfloat16).cuda()
+    v = (size * torch.randn(B, n, 8, 64, generator=g)).to(torch.bfloat16).cuda()
+    pos = torch.tensor([[s + t for t in range(n)] for s in starts], dtype=torch.int32)
+    gqa.paged_append(k, v, pos.cuda(), cache.k, cache.v, cache.table, _int(lengths),
+                     counts=_int(counts), rope=rope, **cache.scales())
+    gqa.check()
+    seen = near = 0
+    for b, (length, c) in enumerate(zip(lengths, counts)):
+        kf, vf = _f64(k[b, :c].float()), _f64(v[b, :c].float())
+        turned = _rotate(kf, pos[b, :c].numpy(), rope) if c else kf
+        for i in range(starts[b] // page, -(-length // page)):
+            lo, hi = max(starts[b], i * page), min(length, (i + 1) * page)
+            if lo >= hi:
+                continue
+            p = int(cache.table_host[b, i])
+            for x, scales, old in ((turned, cache.ks, before[0]), (vf, cache.vs, before[1])):
+                top = np.abs(x[lo - starts[b]:hi - starts[b]]).max(axis=(0, 2))
+                m, _ = np.frexp(top / 448.0)
+                want = np.array([_scale_of(a) for a in top])
+                if lo > i * page:
+                    want = np.maximum(want, _f64(old[p]))
+                got = _f64(scales[p])
+                # within the rotation's error of a border either power may be right
+                border = (np.abs(m - 0.5) < 2.0 ** -19) | (np.abs(m - 1.0) < 2.0 ** -19)
+                border &= x is turned
+                assert np.all((got == want) | border), (b, i, got, want)
+                seen, near = seen + 8, near + int(border.sum())
+    assert near <= seen // 100
