@@ -17,8 +17,8 @@
 // maximum; the warps join at the end.
 //
 // Precision. bf16 pages: q and p are split into two bf16 terms (the second product
-// costs tensor time that HBM leaves unused), so only the sums' fp32 and the output
-// round. e4m3 pages: codes are exact in f16, q is scaled by a power of two per head
+// costs tensor time that HBM leaves unused), which hold 16 bits; beside them only the sums'
+// fp32 and the output round. e4m3 pages: codes are exact in f16, q is scaled by a power of two per head
 // and rounded to f16 (2^-12), and so is p. A page's value scale s_v joins the
 // exponent, w = 2^(x + log2 s_v - M), which keeps w in f16's range whatever the
 // scales are; the normaliser takes w / s_v in fp32.
@@ -271,11 +271,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
         *reinterpret_cast<uint2*>(smem + at) =
             make_uint2(pack_f16x2(y[0] * f, y[1] * f), pack_f16x2(y[2] * f, y[3] * f));
       } else {
-        const uint32_t h0 = pack_bf16x2(y[0], y[1]), h1 = pack_bf16x2(y[2], y[3]);
+        const uint32_t h0 = split_bf16x2(y[0], y[1]), h1 = split_bf16x2(y[2], y[3]);
         *reinterpret_cast<uint2*>(smem + at) = make_uint2(h0, h1);
         *reinterpret_cast<uint2*>(smem + at + NT * kGroup * kHeadDim * 2) =
-            make_uint2(pack_bf16x2(y[0] - bf16lo_to_f32(h0), y[1] - bf16hi_to_f32(h0)),
-                       pack_bf16x2(y[2] - bf16lo_to_f32(h1), y[3] - bf16hi_to_f32(h1)));
+            make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
       }
     }
   }
@@ -450,10 +449,8 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
           if (kFp8) {
             ph[u][tk][h] = transpose8(pack_f16x2(p[2 * h], p[2 * h + 1]));
           } else {
-            const uint32_t w = pack_bf16x2(p[2 * h], p[2 * h + 1]);
-            ph[u][tk][h] = transpose8(w);
-            pl[u][kFp8 ? 0 : tk][h] = transpose8(
-                pack_bf16x2(p[2 * h] - bf16lo_to_f32(w), p[2 * h + 1] - bf16hi_to_f32(w)));
+            ph[u][tk][h] = transpose8(split_bf16x2(p[2 * h], p[2 * h + 1]));
+            pl[u][kFp8 ? 0 : tk][h] = transpose8(pack_bf16x2(p[2 * h], p[2 * h + 1]));
           }
         }
       }

@@ -235,6 +235,19 @@ __device__ __forceinline__ float4 page_factors(float ks, float vs) {
   return make_float4(ks * kScaleLog2, log2f(vs), 1.f / vs, 0.f);
 }
 
+// Splits x and y into two bf16 terms each: returns the first ones, packed, and leaves the
+// second ones, which the caller rounds. Terms of a value have its sign and neither is 0 unless
+// it is: what multiplies them may be infinite, and 0 or terms of two signs would make that
+// NaN. So the first term is cut off, not rounded (together 2^-16 of the value, where a rounded
+// first one leaves 2^-17), and a value of one term gets a second one far below fp32's step.
+__device__ __forceinline__ uint32_t split_bf16x2(float& x, float& y) {
+  const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  const float a = bf16lo_to_f32(hi), b = bf16hi_to_f32(hi);
+  x = a == x ? x * 0x1p-25f : x - a;
+  y = b == y ? y * 0x1p-25f : y - b;
+  return hi;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

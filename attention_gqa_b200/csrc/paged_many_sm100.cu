@@ -194,12 +194,12 @@ __device__ __forceinline__ float store_query(const PagedAttentionArgs& a, uint8_
     uint32_t w[4], v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float y0 = y[8 * c + 2 * e], y1 = y[8 * c + 2 * e + 1];
+      float y0 = y[8 * c + 2 * e], y1 = y[8 * c + 2 * e + 1];
       if (kFp8) {
         w[e] = pack_f16x2(y0 * f, y1 * f);
       } else {
-        w[e] = pack_bf16x2(y0, y1);
-        v[e] = pack_bf16x2(y0 - bf16lo_to_f32(w[e]), y1 - bf16hi_to_f32(w[e]));
+        w[e] = split_bf16x2(y0, y1);
+        v[e] = pack_bf16x2(y0, y1);
       }
     }
     uint8_t* at = row + ((c ^ (r & 7)) << 4);

@@ -410,7 +410,10 @@ size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n, int max_len
  *           uninitialised; calls that overlap in time need separate ones
  * A page number outside [0, num_pages) is reported by check (BAD_PAGE) and read as
  * a page of zeros. What lies in slots that no token sees (later tokens' rows,
- * stale rows, NaN) does not reach the output. Scores, softmax and sums are fp32;
+ * stale rows, NaN) does not reach the output. Infinities in bf16 pages that a token does
+ * see count as such: a score of -inf weighs nothing, one of +inf makes the row NaN, and an
+ * infinite value its element infinite (NaN where its weight is below 2^-100 of the
+ * largest). Scores, softmax and sums are fp32;
  * rotated q and the probabilities keep 16 bits (bf16 pages; with n > 2 the
  * probabilities 8) or 11 bits (e4m3 pages).
  * batch >= 1, n >= 1, batch * n <= 131072. One or two kernels on `stream`. How the work

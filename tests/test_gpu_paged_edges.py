@@ -155,3 +155,62 @@ def test_scales_of_rotated_keys_and_of_pages_used_before(cuda_device, page, rope
                 assert np.all((got == want) | border), (b, i, got, want)
                 seen, near = seen + 8, near + int(border.sum())
     assert near <= seen // 100
+
+
+# -------------------------------------------------------------------- attention
+
+def _check_rows(got, cache, q, sinks, length, window, n):
+    """Attention of one sequence with infinities among what it sees: where the definition gives
+    an infinity or NaN so does the kernel; elsewhere test_gpu_paged's tolerance (of the keys
+    without infinite scores, and the values without infinities)."""
+    r = 2.0 ** -16 if cache.dtype == torch.bfloat16 else 2.0 ** -11
+    rp = 2.0 ** -8 if cache.dtype == torch.bfloat16 and n > 2 else r
+    k, v = cache.sequence(0, length)
+    got = dev_to_f64(got).reshape(n, 64, 64)
+    kz, vz = (np.where(np.isfinite(x), x, 0.0) for x in (k, v))
+    for t in range(n):
+        i = length - n + t
+        turned = _rotate(_f64(q.float())[0, t], i, "plain")
+        with np.errstate(invalid="ignore"):
+            ref, _, _ = _attend(turned, k, v, _f64(sinks), i, window)
+        _, S, V = _attend(turned, kz, vz, _f64(sinks), i, window)
+        assert np.array_equal(np.isnan(got[t]), np.isnan(ref)), t
+        inf = np.isinf(ref)
+        assert np.array_equal(got[t][inf], ref[inf]), t
+        ok = np.isfinite(ref)
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 * V * (2.0 * (r + 2.0 ** -19) * S + rp)
+        assert np.all(np.abs(got[t] - np.where(ok, ref, 0.0))[ok] <= tol[ok]), t
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 20])
+@pytest.mark.parametrize("length,window", [(700, 0), (700, 300), (5000, 0)])
+def test_infinities_that_a_token_sees(cuda_device, n, length, window):
+    """bf16 pages. An infinite key element is a score of one sign or the other: -inf weighs
+    nothing, +inf makes the row NaN. An infinite value makes its element infinite."""
+    page, inf = 32, float("inf")
+    for seed in (0, 1):
+        g = torch.Generator().manual_seed(40 + seed)
+        cache = Cache([length], page, torch.bfloat16)
+        cache.fill([length], g)
+        q, sinks = _queries(1, n, g)
+
+        def put(pages, key, h, d, x):
+            pages[int(cache.table_host[0, key // page]), key % page, h, d] = x
+        if seed == 0:  # keys: in the last tile, inside, before a window
+            put(cache.k, length - 1, 0, 5, inf)
+            put(cache.k, length - n, 1, 33, -inf)
+            put(cache.k, length - 150, 2, 63, inf)
+            put(cache.k, length - 290, 3, 0, -inf)
+            put(cache.k, 1, 4, 17, inf)
+        else:  # values
+            put(cache.v, length - 1, 0, 5, inf)
+            put(cache.v, length - n, 1, 33, -inf)
+            put(cache.v, length - 150, 2, 63, inf)
+            put(cache.v, length - 260, 3, 0, -inf)
+            put(cache.v, 1, 4, 17, inf)
+            put(cache.v, length - 2, 5, 9, inf)
+            put(cache.v, length - 100, 5, 9, -inf)
+        got = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int([length]),
+                                  window=window)
+        gqa.check()
+        _check_rows(got, cache, q, sinks, length, window, n)
