@@ -7,6 +7,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 
 #ifdef __CUDACC__
 #define GQA_HD __host__ __device__ __forceinline__
@@ -121,6 +122,32 @@ GQA_HD uint32_t paged_scale_bits(uint32_t largest_bits) {
   if (e > kScaleHigh) e = kScaleHigh;
   return static_cast<uint32_t>(e + 127) << 23;
 }
+
+// 2^e as fp32, -126 <= e <= 127.
+GQA_HD float paged_power(int e) {
+  const uint32_t bits = static_cast<uint32_t>(e + 127) << 23;
+  float x;
+  memcpy(&x, &bits, sizeof x);
+  return x;
+}
+
+// The unit (a power of two) that a chunk's values are summed in: about the first page's
+// scale. Weights are multiplied by a page's value scale s before they are rounded and
+// summed, w = 2^(x - M) s, and the normaliser takes w / s back. That needs 2^(x - M) s to
+// stay inside fp32's exponents for every x that counts, down to 2^-30 of the largest weight:
+// scales between 2^-76 and 2^20 of the unit leave it above 2^-126. Not below 2^-16, as
+// a first page of zeros has a scale of 2^-64, and says nothing of the others.
+constexpr int kUnitLow = -16, kUnitHigh = 126;
+GQA_HD int paged_unit(float scale) {  // below 0: no scale
+  if (!(scale >= 0.f)) return 0;
+  uint32_t bits;
+  memcpy(&bits, &scale, sizeof bits);
+  const int e = static_cast<int>(bits >> 23) - 127;
+  return e < kUnitLow ? kUnitLow : e > kUnitHigh ? kUnitHigh : e;
+}
+
+// Whether a scale in that unit lies outside.
+GQA_HD bool paged_scale_far(float scale) { return !(scale >= 0x1p-76f && scale <= 0x1p20f); }
 
 // Whether a value (bits of a finite fp32 >= 0) lies within 16 ulps of where its scale
 // changes, 1.75 * 2^x.

@@ -20,8 +20,9 @@
 // costs tensor time that HBM leaves unused), which hold 16 bits; beside them only the sums'
 // fp32 and the output round. e4m3 pages: codes are exact in f16, q is scaled by a power of two per head
 // and rounded to f16 (2^-12), and so is p. A page's value scale s_v joins the
-// exponent, w = 2^(x + log2 s_v - M), which keeps w in f16's range whatever the
-// scales are; the normaliser takes w / s_v in fp32.
+// exponent, w = 2^(x + log2 s_v - M), which keeps the largest w in f16's range whatever
+// the scales are; the normaliser takes w / s_v in fp32. Scales are taken in a chunk's unit (paged.h),
+// and a chunk whose scales are too far apart for that is done again by the formula itself.
 //
 // Bound by HBM where there is much to read, at 256 (bf16) or 128 (e4m3) bytes per key and
 // head: 64 sequences of 8192 in bf16 pages take 166 us, 6.5 TB/s. e4m3 pages need as many
@@ -118,6 +119,8 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
+  volatile int* far = abort_flag + 1;   // e4m3: whether a value scale lies too far from
+  volatile int* unit = abort_flag + 2;  // the chunk's unit
   auto full_bar = [&](int s) { return sbase + L::kBar + 8u * s; };
   auto empty_bar = [&](int s) { return sbase + L::kBar + 8u * (kStages + s); };
   const int warp = static_cast<int>(threadIdx.x >> 5);
@@ -138,8 +141,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
   // The tokens, lengths and pages, and the workspace, may still be in use by
   // the kernel before.
   griddep_wait();
-  if (threadIdx.x == 0)
+  if (threadIdx.x == 0) {
     *abort_flag = (*reinterpret_cast<volatile int*>(a.err) & kErrTimeout) ? 1 : 0;
+    *far = *unit = 0;
+  }
   ScanSlot* slot = reinterpret_cast<ScanSlot*>(smem + L::kScan + 2 * 5 * 4);
   if (!find_chunk<NT, kTile, kThreads>(a, static_cast<int>(blockIdx.x / kNumKvHeads),
                                        reinterpret_cast<uint32_t*>(smem + L::kScan), slot))
@@ -172,6 +177,11 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
       auto fetch = [&](int pi) { return fetch_page<kFp8>(a, table, pi, lo, last_page, g); };
       int pbase = key_a >> page_log2;
       PageEntry cur = fetch(pbase + lane), nxt = fetch(pbase + 32 + lane);
+      int in = 0;  // the chunk's unit
+      if (kFp8) {
+        in = paged_unit(__shfl_sync(0xffffffffu, cur.vs, (max(key_a, lo) >> page_log2) - pbase));
+        if (lane == 0) *unit = in;
+      }
       const int sub = lane & 7;
       int issued = 0;
       int s = 0;             // stage of tile i
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
           const float vs = __shfl_sync(0xffffffffu, cur.vs, (pw - pbase) & 31);
           if (lane < L::kPages)
             *reinterpret_cast<float4*>(smem + L::kPage + (s * L::kPages + lane) * 16) =
-                page_factors(ks, vs);
+                page_factors(ks, vs, in, far);
           __syncwarp();
         }
         if (lane == 0) mbar_arrive(full_bar(s));  // and the scales are there
@@ -520,6 +530,16 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
 
   // ---- join the warps
   named_barrier(1, kWarps * 32);  // every warp has done with the tiles
+  if (kFp8 && *far) {
+    if (skip || *abort_flag) return;
+    const int tokens = min(NT, a.n - t0);
+#pragma unroll 1
+    for (int i = 2 * warp + (lane >> 4); i < tokens * kGroup; i += 2 * kWarps)
+      plain_row(a, b, t0 + i / kGroup, idx0 + i / kGroup, g * kGroup + i % kGroup, key_a,
+                key_a + n_tiles * kTile, chunks,
+                (static_cast<int64_t>(part) * kNumKvHeads + g) * (NT * kGroup) + i);
+    return;
+  }
   float* mo = reinterpret_cast<float*>(smem + L::kMerge + warp * L::kMergeWarp);
 #pragma unroll
   for (int tk = 0; tk < NT; ++tk)
@@ -572,12 +592,14 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
       const float f = ex2_approx(M - Mf);
       const float den = fmaf(f, sum, ex2_approx(sink - Mf));
       const float scale = M > kNoMax ? f / den : 0.f;
+      const float grow = kFp8 ? paged_power(*unit) : 1.f;
       *reinterpret_cast<uint2*>(
           a.out + ((static_cast<int64_t>(b) * a.n + t0 + tk) * kNumHeads + g * kGroup + hh) *
                       kHeadDim + d0) =
-          make_uint2(pack_bf16x2(acc[0] * scale, acc[1] * scale),
-                     pack_bf16x2(acc[2] * scale, acc[3] * scale));
+          make_uint2(pack_bf16x2(acc[0] * scale * grow, acc[1] * scale * grow),
+                     pack_bf16x2(acc[2] * scale * grow, acc[3] * scale * grow));
     } else {
+      if (kFp8) to_part(&M, &sum, acc, *unit);
       const int64_t pr = (static_cast<int64_t>(part) * kNumKvHeads + g) * (NT * kGroup) + r;
       *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + d0) =
           make_float4(acc[0], acc[1], acc[2], acc[3]);

@@ -200,6 +200,26 @@ __device__ __forceinline__ bool find_chunk(const PagedAttentionArgs& a, int cid,
   return slot->row >= 0;
 }
 
+// Four e4m3 codes to two f16x2 words (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+
+// Four e4m3 codes to their values.
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t codes, float (&x)[4]) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16(codes, lo, hi);
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(x[0]), "=f"(x[1])
+      : "r"(lo));
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(x[2]), "=f"(x[3])
+      : "r"(hi));
+}
+
 struct PageEntry {
   int page;
   float ks, vs;
@@ -208,11 +228,11 @@ struct PageEntry {
 // Page `pi` of a sequence and its scales for kv head g. Pages before the one of the
 // first visible key `lo`, or past the last, are not looked at (their entries may be
 // unset); a bad number is reported, and stands for a page past the pool, of which
-// copies read zeros.
+// copies read zeros. Both have a value scale below 0.
 template <bool kFp8>
 __device__ __forceinline__ PageEntry fetch_page(const PagedAttentionArgs& a, const int32_t* table,
                                                 int pi, int lo, int last_page, int g) {
-  PageEntry e = {a.cache.num_pages, 1.f, 1.f};
+  PageEntry e = {a.cache.num_pages, 1.f, -1.f};
   if (pi <= last_page && pi >= (lo >> a.cache.page_log2)) {
     const int page = __ldg(table + pi);
     if (paged_page_ok(page, a.cache.num_pages)) {
@@ -228,11 +248,107 @@ __device__ __forceinline__ PageEntry fetch_page(const PagedAttentionArgs& a, con
   return e;
 }
 
-// What the softmax needs of a page's scales: the factor of its scores, log2 of its
-// value scale, and that scale's reciprocal.
-__device__ __forceinline__ float4 page_factors(float ks, float vs) {
-  vs = fmaxf(vs, 0x1p-100f);
-  return make_float4(ks * kScaleLog2, log2f(vs), 1.f / vs, 0.f);
+// What the softmax needs of a page's scales: the factor of its scores, log2 of its value
+// scale in the chunk's unit (paged.h), and that scale's reciprocal. Sets *far if the scale
+// lies too far from the unit.
+__device__ __forceinline__ float4 page_factors(float ks, float vs, int unit, volatile int* far) {
+  const float v = vs < 0.f ? 1.f : vs * paged_power(-unit);
+  if (paged_scale_far(v)) *far = 1;  // (what the factors make of it is not used)
+  return make_float4(ks * kScaleLog2, log2f(v), 1.f / v, 0.f);
+}
+
+// Normalises a chunk's sums for the joining kernel where values are in a unit: from (M, sum) and
+// elements in 2^unit to the same row with its sum in [1/4, 1/2), so that elements are no
+// larger than the output and overflow only where that does.
+__device__ __forceinline__ void to_part(float* M, float* sum, float (&o)[4], int unit) {
+  if (!(*M > kNoMax)) return;
+  const int k = min(max(static_cast<int>(__float_as_uint(*sum) >> 23) - 127 + 2, -126), 126);
+  *M += static_cast<float>(k);
+  *sum *= paged_power(-k);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = o[e] * paged_power(-k) * paged_power(unit);
+}
+
+// The formula itself, for a chunk with value scales too far apart (e4m3 pages): a half-warp
+// takes one head of one token over the keys [key_a, key_b) that the token sees, lane e of it
+// elements 4e .. 4e+3, and writes the output (the row's only chunk) or its part. Sums are in
+// 64 bits, which hold every product of a weight, a scale and a code. One key after the other,
+// and as slow as such scales are rare. Both half-warps of a warp come with the same token.
+__device__ __forceinline__ void plain_row(const PagedAttentionArgs& a, int b, int t, int idx,
+                                          int head, int key_a, int key_b, int chunks,
+                                          int64_t part_row) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int g = head / kGroup, d0 = (lane & 15) * 4, page_log2 = a.cache.page_log2;
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+  if (idx >= 0) {
+    int p = a.pos ? __ldg(a.pos + static_cast<int64_t>(b) * a.n + t) : idx;
+    p = min(max(p, 0), kMaxPosition - 1);  // (reported by the others)
+    const uint16_t* q = a.q + b * a.q_batch + t * a.q_token + head * kHeadDim;
+    const float2* row = a.rope + static_cast<int64_t>(p) * kRopePairs + (d0 & 31);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __ldg(row + e);
+      const float x = bf16lo_to_f32(__ldg(q + d0 + e)), z = bf16lo_to_f32(__ldg(q + (d0 ^ 32) + e));
+      y[e] = fmaf(x, f.x, (d0 < 32 ? -z : z) * f.y);
+    }
+  }
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+  const int first = a.window > 0 ? max(idx - a.window + 1, key_a) : key_a;
+  const int last = min(idx + 1, key_b);
+  float m = kNoMax;
+  double l = 0., o[4] = {0., 0., 0., 0.};
+#pragma unroll 1
+  for (int key = first; key < last; ++key) {
+    const int page = __ldg(table + (key >> page_log2));
+    uint32_t kc = 0, vc = 0;  // a bad page's
+    float ks = 1.f, vs = 1.f;
+    if (paged_page_ok(page, a.cache.num_pages)) {
+      const int64_t at = page * a.cache.page_stride +
+                         (key & ((1 << page_log2) - 1)) * a.cache.token_stride +
+                         g * a.cache.head_stride + d0;
+      kc = *reinterpret_cast<const uint32_t*>(a.cache.k + at);
+      vc = *reinterpret_cast<const uint32_t*>(a.cache.v + at);
+      ks = __ldg(a.cache.k_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
+      vs = __ldg(a.cache.v_scale + static_cast<int64_t>(page) * kNumKvHeads + g);
+    }
+    float k[4], v[4];
+    e4m3x4_to_f32(kc, k);
+    e4m3x4_to_f32(vc, v);
+    float x = fmaf(y[0], k[0], fmaf(y[1], k[1], fmaf(y[2], k[2], y[3] * k[3])));
+#pragma unroll
+    for (int w = 8; w > 0; w /= 2) x += __shfl_xor_sync(0xffffffffu, x, w);
+    x *= ks * kScaleLog2;
+    if (x > m) {
+      const double f = ex2_approx(m - x);
+      m = x;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= f;
+    }
+    const double p = ex2_approx(x - m);
+    l += p;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += p * (static_cast<double>(vs) * v[e]);
+  }
+  if (chunks == 1) {
+    const float sink = __ldg(a.sinks + head) * kLog2e;
+    const float top = fmaxf(sink, m);
+    const double f = ex2_approx(m - top);
+    const double scale = m > kNoMax ? f / (f * l + ex2_approx(sink - top)) : 0.;
+    *reinterpret_cast<uint2*>(
+        a.out + ((static_cast<int64_t>(b) * a.n + t) * kNumHeads + head) * kHeadDim + d0) =
+        make_uint2(pack_bf16x2(static_cast<float>(o[0] * scale), static_cast<float>(o[1] * scale)),
+                   pack_bf16x2(static_cast<float>(o[2] * scale), static_cast<float>(o[3] * scale)));
+  } else {
+    // as to_part() leaves it
+    const double unit = l > 0. ? 0.25 / l : 1.;
+    *reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + d0) =
+        make_float4(static_cast<float>(o[0] * unit), static_cast<float>(o[1] * unit),
+                    static_cast<float>(o[2] * unit), static_cast<float>(o[3] * unit));
+    if (d0 == 0)
+      a.part_ml[part_row] =
+          m > kNoMax ? make_float2(m + static_cast<float>(log2(4. * l)), 0.25f) : make_float2(m, 0.f);
+  }
 }
 
 // Splits x and y into two bf16 terms each: returns the first ones, packed, and leaves the
@@ -252,14 +368,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// Four e4m3 codes to two f16x2 words (exact).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(codes));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {

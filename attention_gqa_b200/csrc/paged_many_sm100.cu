@@ -20,7 +20,8 @@
 //
 // Precision. bf16 pages: q in two bf16 terms (two products), p in one (2^-8). e4m3
 // pages: codes are exact in f16, and q, scaled by a power of two, and p are f16 (2^-12
-// each); scales of pages enter per 16 columns as in the kernel for few tokens.
+// each); scales of pages enter per 16 columns, in the chunk's unit, as in the kernel for few
+// tokens.
 //
 // Masked values. P is 0 where a query does not see a key, but 0 * NaN is NaN, and in a
 // tile at the edge of what is visible the value rows may be stale or belong to later
@@ -75,7 +76,9 @@ struct Smem {
   static constexpr uint32_t kPage = kRawV + (kFp8 ? kRaw : 0) * kTile8;  // float4 [ring][8]
   static constexpr uint32_t kBar = kPage + (kFp8 ? kPageRing * 8 * 16 : 0);
   static constexpr uint32_t kBad = kBar + 32 * 8;  // [2][2][4] value rows taken out of a tile
-  static constexpr uint32_t kHalfBytes = (kBad + 64 + 1023) / 1024 * 1024;
+  static constexpr uint32_t kUnit = kBad + 64;  // e4m3: whether a value scale lies too far from
+                                                // the chunk's unit; that unit
+  static constexpr uint32_t kHalfBytes = (kUnit + 8 + 1023) / 1024 * 1024;
   static constexpr uint32_t kScan = 2 * kHalfBytes;  // 16 + 16 warp sums, slot
   static constexpr uint32_t kMisc = kScan + 32 * 4 + sizeof(ScanSlot);  // abort flag, TMEM address
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
@@ -234,6 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ht = static_cast<int>(threadIdx.x % kHalf);  // thread and warp of the half
   const int warp = ht >> 5;
   const int lane = ht & 31;
+  volatile int* far = reinterpret_cast<volatile int*>(smem + L::kUnit);
+  volatile int* unit_of = far + 1;
   constexpr int kCtas = kNumKvHeads / 2;  // of a chunk
   const int g = static_cast<int>(blockIdx.x % kCtas) * 2 + half;
 
@@ -296,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(ctx.bar(BAR_RAW_FREE + i), 64);
       }
       fence_barrier_init();
+      *far = *unit_of = 0;
     }
     if (half == 0 && warp == 5) {
       tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -318,6 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n_tiles > 0) {
         cur = fetch(pbase + lane);
         nxt = fetch(pbase + 32 + lane);
+      }
+      int in = 0;  // the chunk's unit
+      if (kFp8 && n_tiles > 0) {
+        in = paged_unit(__shfl_sync(0xffffffffu, cur.vs, (max(key_a, lo) >> page_log2) - pbase));
+        if (lane == 0) *unit_of = in;
       }
       const int sub = lane & 7;
       int issued_k = 0, issued_v = 0;
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float vs = __shfl_sync(0xffffffffu, cur.vs, (pw - pbase) & 31);
           if (lane < 8)
             *reinterpret_cast<float4*>(smem + L::kPage + ((i % kPageRing) * 8 + lane) * 16) =
-                page_factors(ks, vs);
+                page_factors(ks, vs, in, far);
           __syncwarp();
           if (lane == 0) mbar_arrive(ctx.bar(BAR_RAW + s));  // and the scales are there
           issued_k = i + 1;
@@ -739,10 +750,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the row's sums: its output, or a part
       if (ok && n_tiles > 0) ok = ctx.wait_warp(BAR_PV, (n_tiles - 1) & 1);
-      if (ok) {
+      if (kFp8 && ok && *far) {
+        const int tokens = min(kNT, a.n - t0);
+#pragma unroll 1
+        for (int i = 2 * warp + (lane >> 4); i < tokens * kGroup; i += 2 * active)
+          plain_row(a, b, t0 + i / kGroup, idx0 + i / kGroup, g * kGroup + i % kGroup, key_a,
+                    key_a + n_tiles * kTile, chunks,
+                    (static_cast<int64_t>(part) * kNumKvHeads + g) * (kNT * kGroup) + i);
+      } else if (ok) {
         tc_fence_after_sync();
         const bool write = t < a.n;
-        float scale = 1.f;
+        float scale = 1.f, grow = kFp8 ? paged_power(*unit_of) : 1.f;
         if (chunks == 1) {
           const float sink = __ldg(a.sinks + g * kGroup + (r & 7)) * kLog2e;
           const float Mf = fmaxf(sink, m);
@@ -760,18 +778,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(ov[i / 32][i % 32 + 2 * e]) * scale,
-                                 __uint_as_float(ov[i / 32][i % 32 + 2 * e + 1]) * scale);
+              w[e] = pack_bf16x2(__uint_as_float(ov[i / 32][i % 32 + 2 * e]) * scale * grow,
+                                 __uint_as_float(ov[i / 32][i % 32 + 2 * e + 1]) * scale * grow);
             *reinterpret_cast<uint4*>(a.out + orow * kHeadDim + i) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (write) {
+          float M = m, sum = l;
 #pragma unroll
-          for (int i = 0; i < 64; i += 4)
-            *reinterpret_cast<uint4*>(a.part_o + pr * kHeadDim + i) =
-                make_uint4(ov[i / 32][i % 32], ov[i / 32][i % 32 + 1], ov[i / 32][i % 32 + 2],
-                           ov[i / 32][i % 32 + 3]);
-          a.part_ml[pr] = make_float2(m, l);
+          for (int i = 0; i < 64; i += 4) {
+            float o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = __uint_as_float(ov[i / 32][i % 32 + e]);
+            if (kFp8) {
+              M = m, sum = l;
+              to_part(&M, &sum, o, *unit_of);
+            }
+            *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + i) =
+                make_float4(o[0], o[1], o[2], o[3]);
+          }
+          a.part_ml[pr] = make_float2(M, sum);
         }
       }
     }

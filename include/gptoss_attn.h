@@ -324,7 +324,9 @@ int gptoss_attn_decode_noalloc(const void* q, const void* kcache, const void* vc
  * GPTOSS_ATTN_PAGES_BF16: bf16 values; the scales are NULL.
  * GPTOSS_ATTN_PAGES_E4M3: e4m3 codes (4 exponent, 3 mantissa bits, no infinity);
  *   the value is code * scale[p][h], with fp32 scales [num_pages][8] for K and for
- *   V. The append writes powers of two; attention takes any positive finite scale.
+ *   V. The append writes powers of two; attention takes any positive finite scale,
+ *   and is fast where a head's value scales stay within about 2^-76 to 2^20 of that of the
+ *   first page seen (of 2^-16, where that is less).
  */
 enum gptoss_attn_pages { GPTOSS_ATTN_PAGES_BF16 = 0, GPTOSS_ATTN_PAGES_E4M3 = 1 };
 
@@ -415,7 +417,8 @@ size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n, int max_len
  * infinite value its element infinite (NaN where its weight is below 2^-100 of the
  * largest). Scores, softmax and sums are fp32;
  * rotated q and the probabilities keep 16 bits (bf16 pages; with n > 2 the
- * probabilities 8) or 11 bits (e4m3 pages).
+ * probabilities 8) or 11 bits (e4m3 pages, where a value also is off by up to 2^-25 of
+ * its weight's largest product with a value scale, times its code).
  * batch >= 1, n >= 1, batch * n <= 131072. One or two kernels on `stream`. How the work
  * is cut depends on the lengths of the whole batch, and the order of the fp32 sums
  * with it.

@@ -214,3 +214,45 @@ def test_infinities_that_a_token_sees(cuda_device, n, length, window):
                                   window=window)
         gqa.check()
         _check_rows(got, cache, q, sinks, length, window, n)
+
+
+SPREADS = {  # exponent of page i of m
+    "one large": lambda i, m: 119 if i == m // 2 else -64,
+    "one small": lambda i, m: -64 if i == m // 2 else 119,
+    "first small": lambda i, m: -64 if i < 3 else 110,
+    "halves": lambda i, m: -60 if i < m // 2 else 70,
+    "ramp": lambda i, m: -105 + (224 * i) // m,
+    "all small": lambda i, m: -110,
+    "all large": lambda i, m: 119,
+    "moderate": lambda i, m: (-56, 0, 10)[i % 3],
+}
+
+
+@pytest.mark.parametrize("n,lengths", [(1, [400]), (2, [400]), (5, [400, 33]), (20, [600]),
+                                       (1, [5000]), (2, [5000]), (20, [3000])])
+@pytest.mark.parametrize("spread", SPREADS)
+def test_value_scales_far_apart(cuda_device, n, lengths, spread):
+    """Pages whose value scales lie up to 2^224 apart share one softmax: what a small page weighs
+    counts whole, whichever came first, inside a chunk and where chunks are joined."""
+    page = 16
+    g = torch.Generator().manual_seed(50 + n)
+    cache = Cache(lengths, page, E4M3)
+    cache.fill(lengths, g)
+    q, sinks = _queries(len(lengths), n, g)
+    sinks[3::8] = float("-inf")
+    sinks[5::8] = 6.0
+    # the pages of the largest scale hold zeros: the others' values are all there is to see
+    for zeros in (False, True) if spread != "moderate" else (False,):
+        for b, length in enumerate(lengths):
+            m = -(-length // page)
+            for i in range(m):
+                e = SPREADS[spread](i, m)
+                p = int(cache.table_host[b, i])
+                # the largest value stays finite in bf16
+                cache.vs[p] = cache.vs[p].clamp(2.0 ** -9, 2.0 ** -7) * 2.0 ** e
+                if zeros and e == max(SPREADS[spread](j, m) for j in range(m)):
+                    cache.v[p] = torch.zeros_like(cache.v[p].float()).to(E4M3)
+        out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int(lengths),
+                                  **cache.scales())
+        gqa.check()
+        _check_attention(out, cache, q, sinks, lengths, 0)

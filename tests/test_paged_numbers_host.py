@@ -16,6 +16,9 @@ using namespace gqa;
 extern "C" {
 int near_border(unsigned bits) { return paged_near_border(bits); }
 unsigned scale_bits(unsigned bits) { return paged_scale_bits(bits); }
+float power(int e) { return paged_power(e); }
+int unit(float scale) { return paged_unit(scale); }
+int scale_far(float scale) { return paged_scale_far(scale); }
 }
 """
 
@@ -30,6 +33,8 @@ def host(tmp_path_factory):
     lib = ctypes.CDLL(str(so))
     lib.near_border.argtypes = lib.scale_bits.argtypes = [ctypes.c_uint]
     lib.scale_bits.restype = ctypes.c_uint
+    lib.power.restype = ctypes.c_float
+    lib.unit.argtypes = lib.scale_far.argtypes = [ctypes.c_float]
     return lib
 
 
@@ -60,3 +65,20 @@ def test_the_rounded_rotation_stays_within_three_ulps_of_the_pairs_largest(host)
     ulp = np.exp2(np.floor(np.log2(np.maximum(np.abs(lo), np.abs(hi)))) - 23)
     assert np.all(np.abs(plain(a, c, -h, s) - lo) <= 3 * ulp)
     assert np.all(np.abs(plain(h, c, a, s) - hi) <= 3 * ulp)
+
+
+def test_units_of_value_scales(host):
+    inf, nan = float("inf"), float("nan")
+    assert all(host.power(e) == 2.0 ** e for e in range(-126, 128))
+    for scale, unit in ((1.0, 0), (1.99, 0), (0.01, -7), (2.0 ** -16, -16), (2.0 ** -64, -16),
+                        (2.0 ** -149, -16), (0.0, -16), (2.0 ** 120, 120), (3.4e38, 126), (inf, 126),
+                        (-1.0, 0), (nan, 0)):
+        assert host.unit(scale) == unit, scale
+    # what an append writes for a page of zeros is near enough to ordinary scales
+    assert not host.scale_far(2.0 ** -64 * host.power(-host.unit(0.01)))
+    for v, far in ((1.0, 0), (2.0 ** -76, 0), (2.0 ** 20, 0), (2.0 ** -77, 1), (2.0 ** 21, 1), (0.0, 1),
+                   (inf, 1), (nan, 1)):
+        assert host.scale_far(v) == far, v
+    # of two scales of which neither is far, the smaller's weights down to 2^-30 of the largest
+    # stay above fp32's least normal number when the larger holds the running maximum
+    assert 2.0 ** -30 * 2.0 ** -76 / 2.0 ** 20 >= 2.0 ** -126
