@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
 #pragma unroll
         for (int d = 8; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        e = max(-100, min(e, 100));
+        e = max(-126, min(e, 126));
         const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         if (d0 == 0)
           *reinterpret_cast<float*>(smem + L::kQExp + (tk * kGroup + hh) * 4) =

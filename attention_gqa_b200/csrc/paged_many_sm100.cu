@@ -187,7 +187,7 @@ __device__ __forceinline__ float store_query(const PagedAttentionArgs& a, uint8_
 #pragma unroll
     for (int e = 0; e < 64; ++e) top = fmaxf(top, fabsf(y[e]));
     int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-    e = max(-100, min(e, 100));
+    e = max(-126, min(e, 126));
     f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     unit = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   }

@@ -256,3 +256,19 @@ def test_value_scales_far_apart(cuda_device, n, lengths, spread):
                                   **cache.scales())
         gqa.check()
         _check_attention(out, cache, q, sinks, lengths, 0)
+
+
+@pytest.mark.parametrize("n", [1, 2, 5])
+def test_huge_and_tiny_queries_of_e4m3_pages(cuda_device, n):
+    """Queries up to 2^119 and down to 2^-118, against keys that make ordinary scores of them."""
+    page, L = 16, 100
+    g = torch.Generator().manual_seed(60)
+    for e in (100, 110, 116, 118, -100, -110, -118):
+        cache = Cache([L], page, E4M3)
+        cache.fill([L], g)
+        cache.ks.mul_(2.0 ** -e)
+        q, sinks = _queries(1, n, g)
+        q = (q.float().clamp(-1.9, 1.9) * 2.0 ** e).to(torch.bfloat16)
+        out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int([L]), **cache.scales())
+        gqa.check()
+        _check_attention(out, cache, q, sinks, [L], 0)
