@@ -272,3 +272,64 @@ def test_huge_and_tiny_queries_of_e4m3_pages(cuda_device, n):
         out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int([L]), **cache.scales())
         gqa.check()
         _check_attention(out, cache, q, sinks, [L], 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 20])
+@pytest.mark.parametrize("L", [640, 6400])
+def test_maxima_that_move_in_every_tile(cuda_device, dtype, n, L):
+    """Scores that rise by 12 to 25 in the exponent's units from tile to tile and fall back at
+    the end, so that sums and outputs are rescaled again and again, in whole rows and in cut
+    ones, and parts of very different maxima are joined. Scores are exact products (a power of
+    two and a code), so the output's and the weights' roundings are all that is left."""
+    page = 64
+    g = torch.Generator().manual_seed(70)
+    cache = Cache([L], page, dtype, stale=0.0)
+    rise = torch.arange(L // 64, dtype=torch.float32)
+    rise = torch.where(rise > L // 64 - 3, rise - 4, rise)  # the last tiles weigh less
+    # steps of 16 of 256: whole numbers of bf16's and, up to 16 tiles, of e4m3's grid
+    level = (rise % 15 + 1).repeat_interleave(64)
+    k = torch.zeros(1, L, 8, 64)
+    k[:, :, :, 31] = level[None, :, None]
+    k[:, ::7, 1::2, 31] *= 0.5
+    v = torch.randn(1, L, 8, 64, generator=g)
+    zero = torch.zeros(1, L, dtype=torch.int32, device="cuda")
+    gqa.paged_append(k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), zero, cache.k,
+                     cache.v, cache.table, _int([L]), **cache.scales())
+    q = torch.zeros(1, n, 64, 64, dtype=torch.bfloat16, device="cuda")
+    q[:, :, :, 31] = 128.0
+    q[:, :, 1::4, 31] = 64.0
+    q[:, 1::2, 2::4, 31] = -64.0
+    sinks = torch.zeros(64, device="cuda")
+    sinks[::5] = float("-inf")
+    sinks[1::5] = 200.0
+    out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int([L]),
+                              pos=torch.zeros(1, n, dtype=torch.int32, device="cuda"),
+                              **cache.scales())
+    gqa.check()
+    kf, vf = cache.sequence(0, L)
+    rp = 2.0 ** -8 if dtype == torch.bfloat16 and n > 2 else 2.0 ** -11
+    got = dev_to_f64(out)[0]
+    for t in range(n):
+        ref, S, V = _attend(_f64(q[0, t].float()), kf, vf, _f64(sinks), L - n + t, 0)
+        # a score in the exponent is held to 2^-24 of itself, with 2^-22 for the exponential
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 * V * (rp + 2.0 ** -21 * (1.0 + S))
+        err = np.abs(got[t] - ref)
+        assert np.all(err <= tol), (t, (err - tol).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 2, 5, 20])
+@pytest.mark.parametrize("lengths", [[300, 0, 3], [6000, 40, 0]])
+def test_sinks_of_nothing_and_of_everything(cuda_device, dtype, n, lengths):
+    """Sinks of -inf and far above the scores, in whole rows and in joined ones, with rows
+    that see nothing."""
+    g = torch.Generator().manual_seed(80)
+    cache = Cache(lengths, 64, dtype)
+    cache.fill(lengths, g, spread=0.5)
+    q, sinks = _queries(3, n, g)
+    sinks[::3] = float("-inf")
+    sinks[1::6] = 90.0
+    out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int(lengths), **cache.scales())
+    gqa.check()
+    _check_attention(out, cache, q, sinks, lengths, 0)
