@@ -93,11 +93,15 @@ __device__ __forceinline__ const float2* table_row(const PagedAppendArgs& a, int
 }
 
 // Where a sequence's new tokens start and how many there are; a call that does
-// not fit its sequence is reported and appends nothing to it.
+// not fit its sequence is reported and appends nothing to it. Nor does one behind a
+// kernel whose waits timed out: its tokens may be anything, and a page's scale would
+// keep what they were.
 __device__ __forceinline__ bool new_tokens(const PagedAppendArgs& a, int b, int* start,
                                            int* count) {
+  const int err = *a.err;  // (through L1: read past it by every warp, it costs prompts 7 %)
   const int len = __ldg(a.len + b);
   const int c = a.count ? __ldg(a.count + b) : a.n;
+  if (err & kErrTimeout) return false;
   if (!paged_append_ok(len, c, a.n, a.max_len)) {
     atomicOr(a.err, kErrLength);
     return false;

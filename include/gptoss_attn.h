@@ -446,8 +446,8 @@ int gptoss_attn_paged_attention_yarn(const gptoss_attn_paged_cache* cache, const
  * microseconds (1 .. 2000000, else GPTOSS_ATTN_ERR_BAD_SHAPE) the wait gives
  * up, sets the timeout bit of `stream`'s error word and the kernel returns, so
  * the context stays usable. Until gptoss_attn_check(stream) clears the word,
- * prefill, decode and backward kernels launched on `stream` skip their work
- * (other streams are not affected); check then reports
+ * prefill, decode, paged-cache and backward kernels launched on `stream` skip
+ * their work (other streams are not affected); check then reports
  * GPTOSS_ATTN_ERR_DEVICE_TIMEOUT. Asynchronous on `stream`.
  */
 int gptoss_attn_debug_wait_timeout(unsigned timeout_us, cudaStream_t stream);
@@ -456,9 +456,10 @@ int gptoss_attn_debug_wait_timeout(unsigned timeout_us, cudaStream_t stream);
  * Synchronizes `stream`, then reads and clears its error word on the current
  * device (stream-ordered; no other stream is waited on). Returns
  * GPTOSS_ATTN_OK, GPTOSS_ATTN_ERR_DEVICE_TIMEOUT, GPTOSS_ATTN_ERR_BAD_POSITION,
- * GPTOSS_ATTN_ERR_BAD_LENGTH, GPTOSS_ATTN_ERR_BAD_PAGE or GPTOSS_ATTN_ERR_LAUNCH (a CUDA error surfaced
- * by the synchronization). While a stream's word holds a timeout, kernels
- * launched on that stream skip their work.
+ * GPTOSS_ATTN_ERR_BAD_LENGTH, GPTOSS_ATTN_ERR_BAD_PAGE or GPTOSS_ATTN_ERR_LAUNCH (a CUDA
+ * error surfaced by the synchronization). While a stream's word holds a timeout, kernels
+ * launched on that stream skip their work (gptoss_attn_prefill_chunk() still writes its
+ * keys and values to the cache).
  */
 int gptoss_attn_check(cudaStream_t stream);
 

@@ -333,3 +333,32 @@ def test_sinks_of_nothing_and_of_everything(cuda_device, dtype, n, lengths):
     out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int(lengths), **cache.scales())
     gqa.check()
     _check_attention(out, cache, q, sinks, lengths, 0)
+
+
+# ------------------------------------------------------------------- error state
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+def test_append_skips_work_while_a_timeout_is_pending(cuda_device, dtype):
+    """What follows a kernel that gave up leaves the pages and their scales as they are."""
+    lib = gqa._load()
+    g = torch.Generator().manual_seed(95)
+    cache = Cache([40, 7], 16, dtype, stale=0.0)
+    cache.fill([30, 2], g)
+    k = (100.0 * torch.randn(2, 10, 8, 64, generator=g)).to(torch.bfloat16).cuda()
+    pos = torch.zeros(2, 10, dtype=torch.int32, device="cuda")
+    args = (k, k, pos, cache.k, cache.v, cache.table, _int([40, 7]))
+    counts = _int([10, 5])
+    state = [x for x in (cache.k, cache.v, cache.ks, cache.vs) if x is not None]
+    before = [x.clone() for x in state]
+
+    def same():
+        return [torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(state, before)]
+    stream = torch.cuda.current_stream().cuda_stream
+    gqa.check()
+    assert lib.gptoss_attn_debug_wait_timeout(1000, stream) == 0
+    gqa.paged_append(*args, counts=counts, **cache.scales())
+    assert lib.gptoss_attn_check(stream) == -9
+    assert all(same())
+    gqa.paged_append(*args, counts=counts, **cache.scales())
+    gqa.check()
+    assert not any(same())
