@@ -622,9 +622,14 @@ def paged_append(k, v, pos, kpages, vpages, table, lengths, counts=None, kscales
 
 
 @functools.lru_cache(maxsize=256)  # a function of the sizes alone
+def _paged_workspace_bytes(batch: int, n: int, max_len: int, window: int) -> int:
+    return int(_load().gptoss_attn_paged_attention_workspace_bytes(batch, n, max_len, window))
+
+
 def paged_attention_workspace_bytes(batch: int, n: int, max_len: int, window: int = 0) -> int:
-    """Workspace of paged_attention(); 0 where no row of queries can be cut."""
-    return int(_load().gptoss_attn_paged_attention_workspace_bytes(batch, n, max_len, int(window)))
+    """Workspace of paged_attention(): 0 for tables and windows so short that no row of queries
+    can be cut, else no less for a larger batch."""
+    return _paged_workspace_bytes(int(batch), int(n), int(max_len), int(window))
 
 
 def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, pos=None,
@@ -658,7 +663,7 @@ def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, p
     else:
         out_at = _array(out, _BF16, shape, "out", index)
     if workspace is None:
-        need = paged_attention_workspace_bytes(B, n, max_pages * cache.page_size, window)
+        need = _paged_workspace_bytes(B, n, max_pages * cache.page_size, window)
         if need:
             workspace = _empty_on(stream, q, need // 2)
     elif workspace.get_device() != index or not workspace.is_contiguous():

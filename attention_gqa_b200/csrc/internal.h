@@ -205,7 +205,8 @@ struct PagedMaps {
 };
 
 // Query tokens a row holds, how rows are cut (sets most to none_cut), and the workspace
-// for it: none where no row can be cut.
+// for it: none where rows are too short to be cut, and no less for more rows (a workspace of
+// the largest batch serves them all, although very many rows are not cut).
 int paged_row_tokens(int n);
 void paged_plan(PagedAttentionArgs* args);
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]);
