@@ -580,6 +580,14 @@ def _empty_on(stream, like: torch.Tensor, shape) -> torch.Tensor:
     return made
 
 
+def _check_stream(stream, index: int) -> None:
+    """Refuses a stream of another device: its kernels would not be ordered behind what the
+    tensors' device does (a default stream), or not launch at all."""
+    if stream is not None and stream.device_index != index:
+        raise ValueError("stream is of device %d, the tensors are on device %d"
+                         % (stream.device_index, index))
+
+
 def _call_on(index: int, stream, fn, *args) -> int:
     """fn(*args, stream) with device `index` current, on `stream` or its current one."""
     handle = stream.cuda_stream if stream is not None else \
@@ -602,6 +610,7 @@ def paged_append(k, v, pos, kpages, vpages, table, lengths, counts=None, kscales
     index = k.get_device()
     if index < 0:
         raise ValueError("paged_append takes device tensors")
+    _check_stream(stream, index)
     B, n, kb, kt = _heads_at(k, NUM_KV_HEADS, "k", index)
     vB, vn, vb, vt = _heads_at(v, NUM_KV_HEADS, "v", index)
     if vB != B or vn != n:
@@ -643,6 +652,7 @@ def paged_attention(q, kpages, vpages, table, sinks, lengths, window: int = 0, p
     index = q.get_device()
     if index < 0:
         raise ValueError("paged_attention takes device tensors")
+    _check_stream(stream, index)
     single = q.dim() == 3
     B, n, qb, qt = _heads_at(q.unsqueeze(1) if single else q, NUM_HEADS, "q", index)
     cache = _paged_cache(kpages, vpages, kscales, vscales, index)
