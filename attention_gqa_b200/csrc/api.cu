@@ -578,6 +578,7 @@ static int paged_append_impl(const gptoss_attn_paged_cache* cache, const void* k
   a.n = n;
   a.max_pages = max_pages;
   a.max_len = max_pages << a.cache.page_log2;
+  a.num_sms = g_state[dev].num_sms;
   return launch_paged_append(a, stream) == cudaSuccess ? GPTOSS_ATTN_OK : GPTOSS_ATTN_ERR_LAUNCH;
 }
 
@@ -681,7 +682,7 @@ static int paged_attention_impl(const gptoss_attn_paged_cache* cache, const void
   a.n = n;
   a.max_pages = max_pages;
   a.groups = a.rows / batch;
-  paged_plan(&a);
+  paged_plan(&a, g_state[dev].num_sms);
   return launch_paged_attention(maps, a, stream) == cudaSuccess ? GPTOSS_ATTN_OK
                                                                 : GPTOSS_ATTN_ERR_LAUNCH;
 }

@@ -172,6 +172,7 @@ struct PagedAppendArgs {
   const float2* rope;
   int* err;
   int batch, n, max_pages, max_len;
+  int num_sms;
 };
 
 cudaError_t launch_paged_append(const PagedAppendArgs& args, cudaStream_t stream);
@@ -208,7 +209,7 @@ struct PagedMaps {
 // for it: none where rows are too short to be cut, and no less for more rows (a workspace of
 // the largest batch serves them all, although very many rows are not cut).
 int paged_row_tokens(int n);
-void paged_plan(PagedAttentionArgs* args);
+void paged_plan(PagedAttentionArgs* args, int num_sms);
 size_t paged_workspace_bytes(int64_t rows, int n, int max_len, int window, size_t off[3]);
 cudaError_t launch_paged_attention(const PagedMaps& maps, const PagedAttentionArgs& args,
                                    cudaStream_t stream);

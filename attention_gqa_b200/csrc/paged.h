@@ -93,6 +93,19 @@ GQA_HD int64_t paged_max_chunks(int64_t rows, int most, int target) {
 // workspace. Such a row has more than c tiles, so ceil(tiles/c) < 2 tiles/c.
 GQA_HD int64_t paged_max_parts(int target) { return 2 * static_cast<int64_t>(target); }
 
+// Chunks aimed for beyond one wave, by the tokens of a row (for 148 SMs; the workspace is
+// made for so many).
+GQA_HD int paged_target(int row_tokens) { return row_tokens <= 2 ? 111 : 55; }
+
+// Chunks that a GPU of so many SMs holds at a time: eight CTAs of the kernel for few tokens,
+// one per kv head, are a chunk, four of the other. No more than the workspace has parts for.
+GQA_HD int paged_wave(int row_tokens, int num_sms) {
+  const int per_sm = row_tokens == 1 ? 4 : row_tokens == 2 ? 3 : 2;
+  const int parts = static_cast<int>(paged_max_parts(paged_target(row_tokens)));
+  const int wave = num_sms * per_sm / 8;
+  return wave < 1 ? 1 : wave < parts ? wave : parts;
+}
+
 // Tiles [*a, *b) of a row's `tiles` that chunk `i` of `chunks` takes.
 GQA_HD void paged_chunk_range(int tiles, int chunks, int i, int* a, int* b) {
   *a = static_cast<int>(static_cast<int64_t>(tiles) * i / chunks);

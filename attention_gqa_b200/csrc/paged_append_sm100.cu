@@ -374,7 +374,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
     // (four heads in a CTA: 2 x 2048 in pages of 64 6.2 and 8.5 us, 4 x 16384 65 and 55).
     int warps = 1;
     while (warps < kAppendWarps && 8 * warps < most) warps *= 2;
-    if (warps > 1 && static_cast<int64_t>(pages) * a.batch * 8 * warps > 148 * 32) {
+    if (warps > 1 && static_cast<int64_t>(pages) * a.batch * 8 * warps > a.num_sms * 32) {
       warps = 1;
       while (warps < kAppendWarps && 16 * warps < most) warps *= 2;
     }

@@ -159,16 +159,6 @@ cudaError_t launch_paged_combine(const PagedAttentionArgs& a, int row_tokens, cu
 
 int paged_row_tokens(int n) { return n <= 2 ? n : kPagedManyTokens; }
 
-// Chunks that the GPU holds at a time: eight CTAs of the kernel for few tokens, one per kv
-// head, are a chunk, four of the other.
-static int paged_wave(int row_tokens) {
-  const int per_sm = row_tokens == 1 ? 4 : row_tokens == 2 ? 3 : 2;
-  return 148 * per_sm / kNumKvHeads;
-}
-
-// Chunks aimed for beyond one wave.
-static int paged_target(int row_tokens) { return row_tokens <= 2 ? 111 : 55; }
-
 static int paged_most_tiles(int nt, int tile, int max_len, int window) {
   // a row of nt tokens sees window + nt - 1 keys, from anywhere in a tile
   return paged_row_tiles(0, window > 0 && window + nt + tile < max_len ? window + nt + tile : max_len,
@@ -184,10 +174,10 @@ static int paged_most_tiles(int nt, int tile, int max_len, int window) {
 // is known better, so the device estimates whether whole rows end first (36 full rows of
 // 8192 e4m3, five tokens each: 139 us whole, 152 cut; 36 ragged ones: 124 and 103; eight
 // pieces of 40 on 32768: 555 us whole, 397 cut).
-void paged_plan(PagedAttentionArgs* a) {
+void paged_plan(PagedAttentionArgs* a, int num_sms) {
   const int nt = paged_row_tokens(a->n);
   const bool many = nt == kPagedManyTokens;
-  a->wave = paged_wave(nt);
+  a->wave = paged_wave(nt, num_sms);
   a->most = paged_most_tiles(nt, !many && !a->cache.fp8 ? kPagedTile : kPagedTileN, a->max_len,
                              a->window);
   a->none_cut = paged_none_cut(a->rows, a->most);

@@ -16,6 +16,8 @@ using namespace gqa;
 extern "C" {
 int near_border(unsigned bits) { return paged_near_border(bits); }
 unsigned scale_bits(unsigned bits) { return paged_scale_bits(bits); }
+int wave(int row_tokens, int num_sms) { return paged_wave(row_tokens, num_sms); }
+long long max_parts(int row_tokens) { return paged_max_parts(paged_target(row_tokens)); }
 float power(int e) { return paged_power(e); }
 int unit(float scale) { return paged_unit(scale); }
 int scale_far(float scale) { return paged_scale_far(scale); }
@@ -82,3 +84,11 @@ def test_units_of_value_scales(host):
     # of two scales of which neither is far, the smaller's weights down to 2^-30 of the largest
     # stay above fp32's least normal number when the larger holds the running maximum
     assert 2.0 ** -30 * 2.0 ** -76 / 2.0 ** 20 >= 2.0 ** -126
+
+
+def test_a_wave_follows_the_sms_and_fits_the_workspace(host):
+    assert [host.wave(nt, 148) for nt in (1, 2, 16)] == [74, 55, 37]
+    for nt in (1, 2, 16):
+        waves = [host.wave(nt, sms) for sms in (1, 7, 74, 132, 148, 160, 10000)]
+        assert waves == sorted(waves) and waves[0] >= 1 and waves[2] < waves[4] < waves[5]
+        assert waves[-1] == host.max_parts(nt)
