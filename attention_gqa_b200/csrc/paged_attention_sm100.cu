@@ -599,7 +599,11 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 3 : 4)
           make_uint2(pack_bf16x2(acc[0] * scale * grow, acc[1] * scale * grow),
                      pack_bf16x2(acc[2] * scale * grow, acc[3] * scale * grow));
     } else {
-      if (kFp8) to_part(&M, &sum, acc, *unit);
+      if (kFp8) {
+        const float2 f = to_part(&M, &sum, *unit);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f.x * f.y;
+      }
       const int64_t pr = (static_cast<int64_t>(part) * kNumKvHeads + g) * (NT * kGroup) + r;
       *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + d0) =
           make_float4(acc[0], acc[1], acc[2], acc[3]);

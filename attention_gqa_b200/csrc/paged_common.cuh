@@ -257,16 +257,16 @@ __device__ __forceinline__ float4 page_factors(float ks, float vs, int unit, vol
   return make_float4(ks * kScaleLog2, log2f(v), 1.f / v, 0.f);
 }
 
-// Normalises a chunk's sums for the joining kernel where values are in a unit: from (M, sum) and
-// elements in 2^unit to the same row with its sum in [1/4, 1/2), so that elements are no
-// larger than the output and overflow only where that does.
-__device__ __forceinline__ void to_part(float* M, float* sum, float (&o)[4], int unit) {
-  if (!(*M > kNoMax)) return;
+// Normalises a chunk's sums for the joining kernel where values are in a unit: the row's M and
+// sum become those of the same weights with a sum in [1/4, 1/2), and its elements are to be
+// multiplied by both factors returned, one after the other. They are then no
+// larger than the output, and overflow only where that does.
+__device__ __forceinline__ float2 to_part(float* M, float* sum, int unit) {
+  if (!(*M > kNoMax)) return make_float2(1.f, 1.f);
   const int k = min(max(static_cast<int>(__float_as_uint(*sum) >> 23) - 127 + 2, -126), 126);
   *M += static_cast<float>(k);
   *sum *= paged_power(-k);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = o[e] * paged_power(-k) * paged_power(unit);
+  return make_float2(paged_power(-k), paged_power(unit));
 }
 
 // The formula itself, for a chunk with value scales too far apart (e4m3 pages): a half-warp

@@ -760,7 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (ok) {
         tc_fence_after_sync();
         const bool write = t < a.n;
-        float scale = 1.f, grow = kFp8 ? paged_power(*unit_of) : 1.f;
+        float scale = 1.f;
+        const float grow = kFp8 ? paged_power(*unit_of) : 1.f;
         if (chunks == 1) {
           const float sink = __ldg(a.sinks + g * kGroup + (r & 7)) * kLog2e;
           const float Mf = fmaxf(sink, m);
@@ -784,20 +785,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (write) {
-          float M = m, sum = l;
+          const float2 f = kFp8 ? to_part(&m, &l, *unit_of) : make_float2(1.f, 1.f);
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
             float o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = __uint_as_float(ov[i / 32][i % 32 + e]);
-            if (kFp8) {
-              M = m, sum = l;
-              to_part(&M, &sum, o, *unit_of);
+            for (int e = 0; e < 4; ++e) {
+              o[e] = __uint_as_float(ov[i / 32][i % 32 + e]);
+              if (kFp8) o[e] = o[e] * f.x * f.y;
             }
             *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + i) =
                 make_float4(o[0], o[1], o[2], o[3]);
           }
-          a.part_ml[pr] = make_float2(M, sum);
+          a.part_ml[pr] = make_float2(m, l);
         }
       }
     }
