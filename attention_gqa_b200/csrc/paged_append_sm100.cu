@@ -11,10 +11,10 @@
 // range (bf16's largest, times sqrt 2 and YaRN's factor); what it gives is finite all the same.
 //
 // Both kernels have HBM's floor: 256 bytes read per token and kv head, 256 (bf16) or 128
-// (e4m3) written. Measured on a B200 for 4 x 16384 tokens: bf16 43.3 us, 6.2 TB/s of that;
-// e4m3 52 us, 3.9 TB/s, whose CTAs wait in turn for their tokens and for their largest value
-// (64 registers a thread allow 32 warps per SM, and half of the issue slots are used). One
-// token of 64 sequences: 1.7 and 2.6 us on the device, less than a launch.
+// (e4m3) written. Measured on a B200 for 4 x 16384 tokens: bf16 43.5 us, 6.2 TB/s of that;
+// e4m3 51.5 us, 3.9 TB/s, whose CTAs wait in turn for their tokens and for their largest value
+// (64 registers a thread allow 32 warps per SM, and 61 % of the issue slots are used). One
+// token of 64 sequences: 1.7 and 2.7 us on the device, less than a launch.
 #include <cfloat>
 #include <cmath>
 
@@ -195,10 +195,10 @@ constexpr float kWide = 0x1p127f;
 // the CTA that waits for them, the better its waits pass under others' work. Eight lanes
 // take a token, four a head as above (256 bytes in a row); a warp's tokens, at most kTokens to
 // a lane, are read once and kept, for the largest value of each head over the CTA and
-// then for the codes. For 4 x 16384 tokens in pages of 16, 32, 64 and 128: 52, 53, 52 and 56
+// then for the codes. For 4 x 16384 tokens in pages of 16, 32, 64 and 128: 51, 52, 51 and 56
 // us; with four heads in a CTA 51, 50, 54 and 61; with eight 81, 60, 57 and 65; with keys and
 // values in one, 63 to 70 (64); a warp per (page, head) that reads twice, 90 (64). For 7 x
-// 333 in pages of 128: 6.0 us; with four heads 8.3, with eight 13.9.
+// 333 in pages of 128: 6.6 us; with four heads 8.3, with eight 13.9.
 template <int kTokens>
 __global__ void __launch_bounds__(32 * kAppendWarps, 2)
     append_e4m3_kernel(const PagedAppendArgs a) {
@@ -370,8 +370,9 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
     const int P = 1 << a.cache.page_log2;
     const int most = a.n < P ? a.n : P;  // new tokens in one page
     const unsigned pages = static_cast<unsigned>((a.n + P - 2) / P + 1);
-    // Two tokens to a lane while all warps fit the GPU at once (32 to an SM), four beyond
-    // (four heads in a CTA: 2 x 2048 in pages of 64 6.2 and 8.5 us, 4 x 16384 65 and 55).
+    // Two tokens to a lane while all warps fit the GPU at once (32 to an SM), four beyond (2 x
+    // 2048 in pages of 64 6.4 us, and 9.1 with four; 4 x 16384 51 us, and 59 with two. In
+    // between two would still be better by a wave or so: 1 x 8192 9.3 us, 10.5 as it is).
     int warps = 1;
     while (warps < kAppendWarps && 8 * warps < most) warps *= 2;
     if (warps > 1 && static_cast<int64_t>(pages) * a.batch * 8 * warps > a.num_sms * 32) {

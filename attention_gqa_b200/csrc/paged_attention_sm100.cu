@@ -28,8 +28,8 @@
 // head: 64 sequences of 8192 in bf16 pages take 166 us, 6.5 TB/s. e4m3 pages need as many
 // instructions for half the bytes (the conversion of codes has half the rate of other
 // arithmetic), and their warps wait on one another's results: 64 ragged sequences up to
-// 8192 61 us, 4.6 TB/s; one of 131072 33 us, 4.1 TB/s. Short calls are the latency of the
-// lengths, page numbers, tensor maps and pages in turn: one sequence of 257 keys 5.8 us.
+// 8192 62 us, 4.5 TB/s; one of 131072 34 us, 4.0 TB/s. Short calls are the latency of the
+// lengths, page numbers, tensor maps and pages in turn: one sequence of 257 keys 5.9 us.
 //
 // Two tokens at most: with four per row (mma.m16n8k16 for each) five drafted tokens of 16
 // sequences took 142 us and a piece of 512 on 4096 718 us, against 49 and 103 of the

@@ -18,7 +18,9 @@
 //   warps 6-7  look over the value rows of tiles at the edge; e4m3: codes to f16, K and V
 //              of a tile each into its own buffer
 //
-// Precision. bf16 pages: q in two bf16 terms (two products), p in one (2^-8). e4m3
+// Precision. bf16 pages: q in two bf16 terms (two products), p in one (2^-8, as in the prefill
+// kernels: a second term of p has no room beside S and O of both halves in tensor memory, and
+// its store and product would lengthen the chain that bounds the loop). e4m3
 // pages: codes are exact in f16, and q, scaled by a power of two, and p are f16 (2^-12
 // each); scales of pages enter per 16 columns, in the chunk's unit, as in the kernel for few
 // tokens.
@@ -30,9 +32,9 @@
 // them to the queries that see them one by one (exact, and as slow as it is rare).
 //
 // The floor of whole rows is the exponential unit: 128 x 128 of them per tile take 1024
-// cycles of an SM. A pair of halves takes about 3000 for its two tiles, as a row's thread has
+// cycles of an SM. A pair of halves takes about 3800 for its two tiles, as a row's thread has
 // its loads, maximum, exponentials and stores one after the other and only the other
-// half's beside them: 512 tokens on 4096 cached ones take 78 us (bf16; 470 TFLOP/s) and 89
+// half's beside them: 512 tokens on 4096 cached ones take 79 us (bf16; 464 TFLOP/s) and 90
 // (e4m3), of which 32 chunks of 33 to 36 tiles on 37 places. Before the first tile a CTA
 // spends about 5.5 us. Two threads per row, of 64 columns each, which tell each other
 // their maximum, took 96 to 114 us.
