@@ -187,7 +187,7 @@ struct PagedAttentionArgs {
   const int32_t* len;      // [B]
   const float2* rope;
   uint16_t* out;           // [B][n][64][64] bf16
-  float* part_o;           // [part][8][NT * 8][64]: unnormalised sums of a chunk
+  float* part_o;           // [part][8][NT * 8][64]: a chunk's sums, in part_ml's weights
   float2* part_ml;         // [part][8][NT * 8] (max in log2 units, sum)
   int2* meta;              // [rows] (first part, chunks); the three: nullptr if no row is cut
   int* err;

@@ -164,7 +164,8 @@ GQA_HD int paged_unit(float scale) {  // below 0: no scale
 }
 
 // Whether a scale in that unit lies outside.
-GQA_HD bool paged_scale_far(float scale) { return !(scale >= 0x1p-76f && scale <= 0x1p20f); }
+constexpr float kScaleNear = 0x1p-76f;
+GQA_HD bool paged_scale_far(float scale) { return !(scale >= kScaleNear && scale <= 0x1p20f); }
 
 // Whether a value (bits of a finite fp32 >= 0) lies within 16 ulps of where its scale
 // changes, 1.75 * 2^x.

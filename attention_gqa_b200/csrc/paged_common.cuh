@@ -254,7 +254,8 @@ __device__ __forceinline__ PageEntry fetch_page(const PagedAttentionArgs& a, con
 // scale in the chunk's unit (paged.h), and that scale's reciprocal. Sets *far if the scale
 // lies too far from the unit.
 __device__ __forceinline__ float4 page_factors(float ks, float vs, int unit, volatile int* far) {
-  const float v = vs < 0.f ? 1.f : vs * paged_power(-unit);
+  // (zeros have the least scale, so that they do not raise the maximum above the others)
+  const float v = vs < 0.f ? kScaleNear : vs * paged_power(-unit);
   if (paged_scale_far(v)) *far = 1;  // (what the factors make of it is not used)
   return make_float4(ks * kScaleLog2, log2f(v), 1.f / v, 0.f);
 }

@@ -417,8 +417,8 @@ size_t gptoss_attn_paged_attention_workspace_bytes(int batch, int n, int max_len
  * infinite value its element infinite (NaN where its weight is below 2^-100 of the
  * largest). Scores, softmax and sums are fp32;
  * rotated q and the probabilities keep 16 bits (bf16 pages; with n > 2 the
- * probabilities 8) or 11 bits (e4m3 pages, where a value also is off by up to 2^-25 of
- * its weight's largest product with a value scale, times its code).
+ * probabilities 8) or 11 bits (e4m3 pages; they are held times their page's value scale, so
+ * to 2^-25 of the largest such product at least, whatever the other pages' scales).
  * batch >= 1, n >= 1, batch * n <= 131072. One or two kernels on `stream`. How the work
  * is cut depends on the lengths of the whole batch, and the order of the fp32 sums
  * with it.

@@ -362,3 +362,67 @@ def test_append_skips_work_while_a_timeout_is_pending(cuda_device, dtype):
     gqa.paged_append(*args, counts=counts, **cache.scales())
     gqa.check()
     assert not any(same())
+
+
+@pytest.mark.parametrize("n", [1, 2, 5, 20])
+@pytest.mark.parametrize("layout,window", [("token", 0), ("head", 40), ("both", 1)])
+def test_value_scales_far_apart_in_windows_and_odd_places(cuda_device, n, layout, window):
+    """Scales that swing by 2^120 from page to page, with windows, other strides, given
+    positions, rows that see nothing, and a page that is none (zeros, and reported)."""
+    page, lengths = 16, [400, 3, 0, 17]
+    g = torch.Generator().manual_seed(55 + n)
+    cache = Cache(lengths, page, E4M3, layout)
+    cache.fill(lengths, g)
+    for b, length in enumerate(lengths):
+        for i in range(-(-length // page)):
+            cache.vs[int(cache.table_host[b, i])] *= 2.0 ** (60 if i % 2 else -60)
+    q, sinks = _queries(len(lengths), n, g)
+    pos = torch.randint(0, 131072, (len(lengths), n), generator=g, dtype=torch.int32)
+    out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, _int(lengths), window=window,
+                              pos=pos.cuda(), rope="yarn", **cache.scales())
+    gqa.check()
+    _check_attention(out, cache, q, sinks, lengths, window, "yarn", pos)
+    assert not out[2].any()
+    # the last page's number of sequence 3 is out of range: its one key and value are zeros
+    bad = cache.table_host.clone()
+    bad[3, 1] = cache.num
+    got = gqa.paged_attention(q, cache.k, cache.v, bad.cuda(), sinks, _int(lengths), window=window,
+                              pos=pos.cuda(), rope="yarn", **cache.scales())
+    with pytest.raises(gqa.GptossAttnError) as e:
+        gqa.check()
+    assert e.value.status == -12
+    assert torch.equal(got[:3], out[:3])
+    p = int(cache.table_host[3, 1])
+    cache.k[p], cache.v[p] = (torch.zeros(page, 8, 64, device="cuda").to(E4M3) for _ in range(2))
+    _check_attention(got, cache, q, sinks, lengths, window, "yarn", pos, only={3})
+
+
+def test_a_captured_call_follows_scales_that_change(cuda_device):
+    """Replays of one graph over scales near each other, far apart, and near again."""
+    gqa.init()
+    page, lengths = 32, [300, 2000]
+    g = torch.Generator().manual_seed(57)
+    cache = Cache(lengths, page, E4M3)
+    cache.fill(lengths, g)
+    near = cache.vs.clone()
+    graphs = []
+    ln = _int(lengths)
+    for n in (1, 5):
+        q, sinks = _queries(2, n, g)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                out = gqa.paged_attention(q, cache.k, cache.v, cache.table, sinks, ln, **cache.scales())
+        graphs.append((graph, q, sinks, out))
+    torch.cuda.synchronize()
+    for factor in (1.0, 2.0 ** 90, 1.0, 2.0 ** -90, 2.0 ** 3):
+        cache.vs.copy_(near)
+        cache.vs[::2] *= factor
+        for graph, q, sinks, out in graphs:
+            graph.replay()
+            gqa.check()
+            _check_attention(out, cache, q, sinks, lengths, 0)
+    for graph, *_ in graphs:
+        graph.reset()
