@@ -583,9 +583,9 @@ def _empty_on(stream, like: torch.Tensor, shape) -> torch.Tensor:
 def _check_stream(stream, index: int) -> None:
     """Refuses a stream of another device: its kernels would not be ordered behind what the
     tensors' device does (a default stream), or not launch at all."""
-    if stream is not None and stream.device_index != index:
-        raise ValueError("stream is of device %d, the tensors are on device %d"
-                         % (stream.device_index, index))
+    at = getattr(stream, "device_index", index)  # (any object with a handle will do)
+    if at != index:
+        raise ValueError("stream is of device %d, the tensors are on device %d" % (at, index))
 
 
 def _call_on(index: int, stream, fn, *args) -> int:

@@ -54,3 +54,10 @@ def test_a_stream_of_another_device_is_refused():
         gqa.paged_append(x, x, x, x, x, x, x, stream=OtherDevicesStream())
     with pytest.raises(ValueError, match="stream is of device 1"):
         gqa.paged_attention(x, x, x, x, x, x, stream=OtherDevicesStream())
+
+
+def test_an_object_with_a_handle_is_a_stream():
+    class Handle:
+        cuda_stream = 7
+    gqa._check_stream(Handle(), 0)
+    gqa._check_stream(None, 0)
